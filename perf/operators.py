@@ -95,7 +95,7 @@ def draw(rng):
         return dict(op=op, B=B, Hkv=Hkv, D=D, lo=max(1, hi // rng.randint(1, 8)), hi=hi,
                     cap=_cap(hi))
     # new tokens, all sequences together; many heads get fewer of them
-    tokens = _spread(rng, 1, min(12000, 640000 // (Hkv * (g + 2))))
+    tokens = _spread(rng, 1, min(12000, 620000 // (Hkv * (g + 2))))
     B = _spread(rng, 1, min(64, tokens))
     T = max(1, tokens // B)
     lo, hi = (0, 0) if op == "append_bwd" else (0, rng.randint(0, 400))
