@@ -38,7 +38,8 @@
  *     GQA_DEV_* bits into (NULL: device-side errors are not reported).  The
  *     caller zeroes it and reads it after synchronising.
  *   - RoPE pairs coordinate i with i + D/2 and turns pair i at position p by
- *     p * base^(-2i/D) radians; QK-RMSNorm (unit gain) runs before RoPE.
+ *     p * base^(-2i/D) radians; QK-RMSNorm (unit gain, or learned gains in the
+ *     gqa_norm_rope_* calls) runs before RoPE.
  *   - scale <= 0 selects 1/sqrt(D).
  *   - Every element written is a bf16 rounded to nearest even from fp32 math.
  */
@@ -305,6 +306,143 @@ gqa_status gqa_decode_noalloc(const void *q, const void *k_cache, const void *v_
                               const int32_t *lens, int max_len_host, void *out, int B, int Hq,
                               int Hkv, int D, int Lmax, float scale, int32_t *status_dev,
                               void *stream);
+
+/*
+ * Learned gains and positions of several axes, for the gqa_norm_rope_* calls.
+ *   q_gain, k_gain: bf16 [D], multiplied onto the normalised q and k before they
+ *     turn (NULL: ones).  They need qk_norm.
+ *   pos: int32 [n_axes, B, T], the position of every token on every axis (image
+ *     and video tokens: time, height, width), or NULL for pos0[b] + t.  Only the
+ *     angles follow pos: cache slots are pos0[b] + t in either case.  Positions
+ *     may be any int32; those of tokens t >= n_tok[b] are not read.
+ *   pair_axis: the axis, 0 .. n_axes - 1, by which rotation pair i (coordinates
+ *     i and i + D/2) turns, for i < D/2.  Read only with pos.
+ * A NULL gqa_rope_inputs means no gains and positions pos0[b] + t; the results
+ * are then those of gqa_rope_append.
+ */
+#define GQA_MAX_AXES 4
+
+typedef struct {
+    const void *q_gain, *k_gain;
+    const int32_t *pos;
+    int n_axes;                 /* 1 .. GQA_MAX_AXES */
+    uint8_t pair_axis[64];
+} gqa_rope_inputs;
+
+/*
+ * gqa_norm_rope_append -- gqa_rope_append with learned gains, positions on up to
+ * four axes, a separate output for q and per-sequence token counts.  With
+ *     u = gain * x * (mean(x^2) + eps)^(-1/2)     (x itself without qk_norm)
+ *     y(x) = mscale * (pair i of u turned by P_i theta_i)
+ * and P_i the token's position on pair i's axis, for every t < n_tok[b]:
+ *     q_out[b, t, h, :]              = y(q[b, t, h, :])
+ *     k_cache[b, h, pos0[b] + t, :]  = y(k[b, t, h, :])
+ *     v_cache[b, h, pos0[b] + t, :]  = v[b, t, h, :]      (bit copy)
+ * Rows t >= n_tok[b] of q_out and every other cache slot are left as they were.
+ *   q, q_out: [B, T, Hq, D]; q_out may be q.  q NULL: K and V only (Hq, q_out
+ *     are then not used).
+ *   pos0: device int32 [B], or NULL for 0.  n_tok: device int32 [B] (0 .. T), or
+ *     NULL for T everywhere.  A sequence with pos0[b] < 0 or n_tok[b] outside
+ *     0 .. T raises GQA_DEV_BAD_LEN, one with pos0[b] + n_tok[b] > Lmax
+ *     GQA_DEV_CAPACITY; nothing of it is written, its q rows included.
+ *   max_pos0_host: host-known upper bound of pos0 (-1: none).  Without n_tok,
+ *     max_pos0_host + T > Lmax is GQA_ERR_CAPACITY.
+ *   new_len: optional device int32 [B] output, pos0[b] + n_tok[b] (pos0[b] where
+ *     n_tok[b] is out of range).  It must be neither pos0 nor n_tok.
+ */
+gqa_status gqa_norm_rope_append(const void *q, const void *k, const void *v, void *q_out,
+                                void *k_cache, void *v_cache, const int32_t *pos0,
+                                const int32_t *n_tok, int max_pos0_host, int32_t *new_len,
+                                int B, int T, int Hq, int Hkv, int D, int Lmax,
+                                gqa_rope_params p, const gqa_rope_inputs *x,
+                                int32_t *status_dev, void *stream);
+
+/*
+ * gqa_norm_rope_append_backward -- the gradients of gqa_norm_rope_append (without
+ * n_tok): from dq_out [B, T, Hq, D] and the gradients of the cache slots
+ * pos0[b] .. pos0[b] + T - 1, dk_cache and dv_cache [B, Hkv, Lmax, D] (what
+ * gqa_attention_backward leaves), to those of q, k, v and the gains.  With
+ * r = (mean(x^2) + eps)^(-1/2), w = mscale R(P)^T dy and z = gain * w:
+ *     dx = r z - x r^3 mean(x z)     (dx = w without qk_norm)
+ *     d gain = sum over b, t, h of w x r
+ *     dv[b, t, h, :] = dv_cache[b, h, pos0[b] + t, :]
+ *   q, k: the forward's inputs (not its outputs).  dq, dk, dv: bf16, the shapes
+ *     of q, k and v; dq may be dq_out.  dq_gain, dk_gain: float32 [D] outputs
+ *     (NULL: not wanted); they need qk_norm, not a gain in x (the gradient at
+ *     gain one is then meant).
+ *   ws, ws_bytes: device scratch of gqa_norm_rope_backward_workspace_bytes(D)
+ *     bytes, 16-byte aligned, when a gain gradient is wanted; contents on entry
+ *     do not matter.  Calls that may run at the same time must not share one.
+ * Gain gradients are summed in a fixed order: equal calls give equal bits.  A
+ * sequence whose pos0[b] is out of range raises the forward's bits, its rows of
+ * dq, dk and dv are left as they were and it adds nothing to the gains'.
+ */
+gqa_status gqa_norm_rope_append_backward(const void *q, const void *k, const void *dq_out,
+                                         const void *dk_cache, const void *dv_cache, void *dq,
+                                         void *dk, void *dv, float *dq_gain, float *dk_gain,
+                                         const int32_t *pos0, int max_pos0_host, int B, int T,
+                                         int Hq, int Hkv, int D, int Lmax, gqa_rope_params p,
+                                         const gqa_rope_inputs *x, void *ws, size_t ws_bytes,
+                                         int32_t *status_dev, void *stream);
+
+/* Bytes of workspace for gain gradients at head dimension D (0 on invalid D). */
+size_t gqa_norm_rope_backward_workspace_bytes(int D);
+
+/*
+ * The 4-bit cache.  A row (one token of one KV head, D values) has D/32 groups of
+ * 32 values; group G is coordinates 16 G .. 16 G + 15 and D/2 + the same (both
+ * members of 16 rotation pairs).  A group keeps m = min x and
+ * s = bf16((max x - m) / 15), and each value a code c = ceil((x - m) / s - 1/2)
+ * in 0 .. 15 that stands for m + s c.  (A quotient less than 2^-19 of itself above
+ * n + 1/2 may get n.)  s below 2^-126 is kept as 0: every value is m.  A group with
+ * a value that is not finite reads back as NaN throughout.
+ *   k_codes, v_codes   uint8 [B, Hkv, Lmax, D/2]: pair p's byte, coordinate p in
+ *       its low half and p + D/2 in its high half, is byte
+ *       4 * (D/32 * ((p % 16) / 4) + p / 16) + p % 4 of the row.
+ *   k_scales, v_scales bf16 [B, Hkv, Lmax, D/32, 2]: (s, m) of each group.
+ * Rows behind a sequence's length may hold anything.
+ *
+ * gqa_norm_rope_append_q4 -- gqa_norm_rope_append into a 4-bit cache: the K rows
+ * quantised are the bf16 values that the bf16 cache would hold.  Arguments,
+ * errors and what is left alone as there.
+ */
+gqa_status gqa_norm_rope_append_q4(const void *q, const void *k, const void *v, void *q_out,
+                                   void *k_codes, void *k_scales, void *v_codes, void *v_scales,
+                                   const int32_t *pos0, const int32_t *n_tok, int max_pos0_host,
+                                   int32_t *new_len, int B, int T, int Hq, int Hkv, int D,
+                                   int Lmax, gqa_rope_params p, const gqa_rope_inputs *x,
+                                   int32_t *status_dev, void *stream);
+
+/*
+ * kv_cache_read_q4 -- slots first[b] .. first[b] + count[b] - 1 of a 4-bit cache as
+ * bf16 rows (m + s c rounded once), e.g. the prefix that gqa_prefill_chunk reads:
+ *     k_out[b, h, i, :] = K[b, h, first[b] + i, :],  V likewise,  i < count[b];
+ * k_out, v_out [B, Hkv, Lout, D]; rows i >= count[b] are left as they were.
+ *   first: device int32 [B], or NULL for 0.  count: device int32 [B], or NULL for
+ *     Lout everywhere.  Negative values raise GQA_DEV_BAD_LEN, count[b] > Lout or
+ *     first[b] + count[b] > Lmax GQA_DEV_CAPACITY; nothing of that sequence is
+ *     written.
+ */
+gqa_status kv_cache_read_q4(const void *k_codes, const void *k_scales, const void *v_codes,
+                            const void *v_scales, const int32_t *first, const int32_t *count,
+                            void *k_out, void *v_out, int B, int Hkv, int D, int Lmax, int Lout,
+                            int32_t *status_dev, void *stream);
+
+/*
+ * gqa_decode_q4 -- gqa_decode against a 4-bit cache; K and V are the values
+ * m + s c, not rounded to bf16.  Lengths, errors and the workspace's rules as
+ * there; gqa_decode_q4_workspace_bytes gives its size (a cut of the sequences that
+ * needs no merge wants none; 16 bytes are named then).  Values of magnitude up to
+ * 2^110 are handled (sums of larger ones can overflow).
+ */
+gqa_status gqa_decode_q4(const void *q, const void *k_codes, const void *k_scales,
+                         const void *v_codes, const void *v_scales, const int32_t *lens,
+                         int max_len_host, void *out, int B, int Hq, int Hkv, int D, int Lmax,
+                         float scale, void *ws, size_t ws_bytes, int32_t *status_dev,
+                         void *stream);
+
+/* Bytes of workspace gqa_decode_q4 needs for these sizes (0 on invalid sizes). */
+size_t gqa_decode_q4_workspace_bytes(int B, int Hq, int Hkv, int D, int max_len);
 
 /*
  * gqa_selftest_bounded_wait -- checks the bounded waits without a fault, through

@@ -15,7 +15,7 @@ extern "C" const char *gqa_status_string(gqa_status s) {
     return "unknown status";
 }
 
-extern "C" int gqa_version(void) { return 200; }
+extern "C" int gqa_version(void) { return 300; }
 
 // One thread waits on an mbarrier that nothing arrives on, through
 // ptx::mbar_wait -- the function every kernel of the library waits with -- with

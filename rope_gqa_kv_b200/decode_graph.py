@@ -13,7 +13,10 @@ two device vectors -- the append reads one as the new token's position and
 writes the other (length + 1), which the decode then reads -- so two graphs,
 one for each direction, cover every step, and no host value changes between
 replays.  The decode's grid covers ``max_len`` cache slots (default: the whole
-capacity); the CTAs past a sequence's current length exit at once.
+capacity); the CTAs past a sequence's current length exit at once.  With a 4-bit
+cache, learned gains or several position axes the append is
+``gqa_norm_rope_append`` or ``gqa_norm_rope_append_q4``, and a 4-bit cache is read
+by ``gqa_decode_q4``.
 """
 from __future__ import annotations
 
@@ -31,11 +34,21 @@ class DecodeGraph:
     the first step; :attr:`lens` is the current length vector.  The caches are
     updated in place, exactly as by the eager calls.  Device errors are OR-ed
     into ``status``.
+
+    ``k_cache`` may be a ``Q4Cache`` (``v_cache`` is then None).  ``q_gain`` and
+    ``k_gain`` (bfloat16 [D]) are learned gains of the norm; they are read at every
+    step.  With ``axes`` (a ``RopeAxes``), write the new token's position on every
+    axis into ``pos`` (int32 [n_axes, B]) before each step; without, it is the
+    cached length.
     """
 
     def __init__(self, k_cache, v_cache, lens, Hq, max_len=None, qk_norm=False, eps=1e-6,
-                 rope_base=10000.0, scaling=None, scale=0.0):
-        if not (isinstance(k_cache, torch.Tensor) and k_cache.is_cuda):
+                 rope_base=10000.0, scaling=None, scale=0.0, q_gain=None, k_gain=None,
+                 axes=None):
+        q4 = isinstance(k_cache, _lib.Q4Cache)
+        if q4 and v_cache is not None:
+            raise ValueError("a Q4Cache holds K and V: v_cache must be None")
+        if not q4 and not (isinstance(k_cache, torch.Tensor) and k_cache.is_cuda):
             raise ValueError("k_cache must be a CUDA tensor (no CPU path exists)")
         B, Hkv, Lmax, D = k_cache.shape
         dev = k_cache.device
@@ -48,14 +61,33 @@ class DecodeGraph:
         self.status = torch.zeros(1, dtype=torch.int32, device=dev)
         self._lens = [lens.to(device=dev, dtype=torch.int32).clone(),
                       lens.to(device=dev, dtype=torch.int32).clone()]
-        self._workspace = _lib.decode_workspace(B, Hq, D, self.max_len, dev)
+        self.pos = None if axes is None else torch.zeros(axes.n_axes, B, dtype=torch.int32,
+                                                         device=dev)
         rope = dict(qk_norm=qk_norm, eps=eps, rope_base=rope_base, scaling=scaling)
+        learned = dict(q_gain=q_gain, k_gain=k_gain, pos=self.pos, axes=axes)
+        q_rot = torch.empty_like(self.q)        # the learned-norm appends leave q as it is
+        # The graphs hold addresses only: what they read and write stays alive with them.
+        self._held = (k_cache, v_cache, q_gain, k_gain, q_rot)
+        if q4:
+            self._workspace = _lib.decode_q4_workspace(B, Hq, Hkv, D, self.max_len, dev)
+        else:
+            self._workspace = _lib.decode_workspace(B, Hq, D, self.max_len, dev)
 
         def one_step(a, b):
-            _lib.gqa_rope_append(self.q, self.k, self.v, k_cache, v_cache, pos0=self._lens[a],
-                                 new_len=self._lens[b], status=self.status, **rope)
-            _lib.gqa_decode(self.q, k_cache, v_cache, self._lens[b], self.max_len, out=self.out,
-                            workspace=self._workspace, scale=scale, status=self.status)
+            args = dict(pos0=self._lens[a], new_len=self._lens[b], status=self.status, **rope)
+            tail = dict(out=self.out, workspace=self._workspace, scale=scale, status=self.status)
+            if q4:
+                _lib.gqa_norm_rope_append_q4(self.q, self.k, self.v, k_cache, q_out=q_rot,
+                                             **learned, **args)
+                _lib.gqa_decode_q4(q_rot, k_cache, self._lens[b], self.max_len, **tail)
+                return
+            if q_gain is None and k_gain is None and axes is None:
+                _lib.gqa_rope_append(self.q, self.k, self.v, k_cache, v_cache, **args)
+                _lib.gqa_decode(self.q, k_cache, v_cache, self._lens[b], self.max_len, **tail)
+                return
+            _lib.gqa_norm_rope_append(self.q, self.k, self.v, k_cache, v_cache, q_out=q_rot,
+                                      **learned, **args)
+            _lib.gqa_decode(q_rot, k_cache, v_cache, self._lens[b], self.max_len, **tail)
 
         # One eager step first, on a side stream, so that every first-use setup
         # (kernel attributes, the library load) happens outside the capture.  It
