@@ -9,6 +9,7 @@ library or a CPU tensor raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -16,6 +17,7 @@ import torch
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libgqa.so")
 _lib = None
+_fast_pointers = None                  # csrc/fastargs.c, set by load()
 
 GQA_OK = 0
 GQA_DEV_CAPACITY = 0x1
@@ -78,7 +80,9 @@ class RopeAxes:
             raise ValueError("axes are 0 .. %d" % (MAX_AXES - 1))
         if set(self.pairs) != set(range(self.n_axes)):
             raise ValueError("every axis needs at least one pair")
-        self._array = (ctypes.c_uint8 * 64)(*self.pairs)
+        x = RopeInputs(n_axes=self.n_axes)
+        x.pair_axis[:len(self.pairs)] = self.pairs
+        self._inputs = bytes(x)        # what a call copies and puts its pointers into
 
 
 class Q4Cache:
@@ -86,17 +90,20 @@ class Q4Cache:
     scales bf16 [B, Hkv, Lmax, D/32, 2] of K and of V.  :meth:`zeros` makes one."""
 
     def __init__(self, k_codes, k_scales, v_codes, v_scales):
-        _need(k_codes, "k_codes", torch.uint8, 4)
-        B, Hkv, Lmax, half = k_codes.shape
+        if not isinstance(k_codes, torch.Tensor):
+            raise TypeError("k_codes must be a torch.Tensor")
+        if k_codes.dim() != 4 or k_codes.shape[3] not in (32, 48, 64):
+            raise ValueError("k_codes must be [B, Hkv, Lmax, D/2] with D 64, 96 or 128, got %s" %
+                             (tuple(k_codes.shape),))
+        B, Hkv, Lmax, half = self._codes_shape = tuple(k_codes.shape)
         self.device, self.shape = k_codes.device, (B, Hkv, Lmax, 2 * half)
-        if half not in (32, 48, 64):
-            raise ValueError("k_codes must be [B, Hkv, Lmax, D/2] with D 64, 96 or 128")
-        scales = (B, Hkv, Lmax, half // 16, 2)
-        _exact(k_scales, "k_scales", torch.bfloat16, scales, self.device)
-        _exact(v_codes, "v_codes", torch.uint8, k_codes.shape, self.device)
-        _exact(v_scales, "v_scales", torch.bfloat16, scales, self.device)
+        self._scales_shape = (B, Hkv, Lmax, half // 16, 2)
         self.k_codes, self.k_scales = k_codes, k_scales
         self.v_codes, self.v_scales = v_codes, v_scales
+        for part in (k_codes, k_scales, v_codes, v_scales):
+            if part is None:
+                raise TypeError("a Q4Cache needs its four tensors")
+        _pointers(self.device, self._spec())
 
     @classmethod
     def zeros(cls, B, Hkv, Lmax, D, device="cuda"):
@@ -106,8 +113,13 @@ class Q4Cache:
                   for _ in range(2)]
         return cls(codes[0], scales[0], codes[1], scales[1])
 
-    def _ptrs(self):
-        return _ptr(self.k_codes), _ptr(self.k_scales), _ptr(self.v_codes), _ptr(self.v_scales)
+    def _spec(self):
+        """The cache's part of a call's tensors, for _pointers."""
+        codes, scales = self._codes_shape, self._scales_shape
+        return ("k_codes", self.k_codes, torch.uint8, codes,
+                "k_scales", self.k_scales, torch.bfloat16, scales,
+                "v_codes", self.v_codes, torch.uint8, codes,
+                "v_scales", self.v_scales, torch.bfloat16, scales)
 
 
 SIGNATURES = {
@@ -153,7 +165,7 @@ class GqaError(RuntimeError):
 
 def load(path: str | None = None):
     """Load libgqa.so (raises if it is missing: there is no fallback)."""
-    global _lib
+    global _lib, _fast_pointers
     if _lib is None:
         p = path or LIB_PATH
         if not os.path.exists(p):
@@ -164,6 +176,15 @@ def load(path: str | None = None):
             fn = getattr(lib, name)
             fn.restype = res
             fn.argtypes = args
+        try:
+            from . import _fastargs
+        except ImportError as e:
+            raise RuntimeError("the binding's argument checks (_fastargs.so) are not built; "
+                               "build them with `python -m rope_gqa_kv_b200.build`") from e
+        _fastargs.setup(torch.Tensor.__dlpack_c_exchange_api__, (
+            (torch.bfloat16, 4, 16), (torch.int32, 0, 32), (torch.uint8, 1, 8),
+            (torch.float32, 2, 32)))
+        _fast_pointers = _fastargs.pointers
         _lib = lib
     return _lib
 
@@ -200,25 +221,36 @@ def _need(t, name, dtype, ndim=None):
         raise ValueError("%s must have %d dims, got %s" % (name, ndim, tuple(t.shape)))
 
 
-def _exact(t, name, dtype, shape, dev):
-    """_need, plus the exact shape and the device of the call's first tensor."""
-    _need(t, name, dtype)
-    if t.shape != tuple(shape):
-        raise ValueError("%s must be %s, got %s" % (name, tuple(shape), tuple(t.shape)))
-    if t.device != dev:
-        raise ValueError("%s is on %s, expected %s" % (name, t.device, dev))
+def _pointers(dev, spec):
+    """Data pointers of a call's tensors (0 for None) and, last, dev's current stream.
 
-
-def _optional(t, name, dtype, shape, dev):
-    if t is not None:
-        _exact(t, name, dtype, shape, dev)
-
-
-def _status_word(status, dev):
-    if status is not None:
-        _need(status, "status", torch.int32)
-        if status.numel() < 1 or status.device != dev:
-            raise ValueError("status must be an int32 word on %s" % dev)
+    spec = (name, tensor, dtype, shape, name, tensor, ...): every tensor must be a
+    contiguous CUDA tensor on dev of that dtype and shape (None: any shape of at least
+    one element).  csrc/fastargs.c says whether they are; what it does not accept is
+    looked at here, one by one, to be refused by name."""
+    if dev.type != "cuda":
+        raise ValueError("%s must be a CUDA tensor (no CPU path exists)" % spec[0])
+    if _fast_pointers is None:
+        load()
+    ptrs = _fast_pointers(dev.index, spec)
+    if ptrs is not None:
+        return ptrs
+    ptrs = []
+    for i in range(0, len(spec), 4):
+        name, t, dtype, shape = spec[i:i + 4]
+        if t is None:
+            ptrs.append(0)
+            continue
+        _need(t, name, dtype)
+        if shape is not None and t.shape != tuple(shape):
+            raise ValueError("%s must be %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+        if t.numel() < 1:
+            raise ValueError("%s is empty" % name)
+        if t.device != dev:
+            raise ValueError("%s is on %s, expected %s" % (name, t.device, dev))
+        ptrs.append(t.data_ptr())
+    ptrs.append(torch.cuda.current_stream(dev).cuda_stream)
+    return ptrs
 
 
 def _new(stream, make):
@@ -229,53 +261,74 @@ def _new(stream, make):
         return make()
 
 
-def _launch(name, dev, stream, *args):
-    """Calls the library on device `dev`, whichever is current, with the stream (the
-    device's current one by default) as the last argument."""
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    elif stream.device != dev:
-        raise ValueError("the stream is on %s, the tensors are on %s" % (stream.device, dev))
-    fn = getattr(load(), name)
+def _launch(name, dev, stream, current, *args):
+    """Calls the library on device `dev`, whichever is current, with the stream (by
+    default the handle `current`, dev's current one) as the last argument."""
+    if stream is not None:
+        if stream.device != dev:
+            raise ValueError("the stream is on %s, the tensors are on %s" % (stream.device, dev))
+        current = stream.cuda_stream
+    fn = getattr(_lib, name)
     if torch.cuda.current_device() == dev.index:
-        _check(name, fn(*args, ctypes.c_void_p(stream.cuda_stream)))
+        st = fn(*args, current)
     else:
         with torch.cuda.device(dev):
-            _check(name, fn(*args, ctypes.c_void_p(stream.cuda_stream)))
+            st = fn(*args, current)
+    if st != GQA_OK:
+        raise GqaError(name, st)
 
 
-def _rope_inputs(B, T, D, q_gain, k_gain, pos, axes, qk_norm, dev):
-    """The gqa_rope_inputs of a call, or None where nothing of it is used."""
+def _need_tensor(t, name):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+
+
+def _pos_shape(pos, axes, B, T, D):
+    """The shape that pos must have."""
+    if axes is not None and len(axes.pairs) != D // 2:
+        raise ValueError("axes cover %d rotation pairs, D = %d has %d" %
+                         (len(axes.pairs), D, D // 2))
+    _need_tensor(pos, "pos")
+    n = 1 if axes is None else axes.n_axes
+    if pos.dim() != 2:
+        return (n, B, T)
+    if T == 1 and (n > 1 or pos.shape[0] == 1):
+        return (n, B)
+    return (B, T) if n == 1 else (n, B, T)
+
+
+def _rope_spec(B, T, D, q_gain, k_gain, pos, axes, qk_norm):
+    """Gains and positions as the last three tensors of a call's spec."""
     if axes is not None and pos is None:
         raise ValueError("axes need pos, the positions on every axis")
-    if q_gain is None and k_gain is None and pos is None:
-        return None
-    if (q_gain is not None or k_gain is not None) and not qk_norm:
+    if not qk_norm and (q_gain is not None or k_gain is not None):
         raise ValueError("q_gain and k_gain need qk_norm=True")
-    _optional(q_gain, "q_gain", torch.bfloat16, (D,), dev)
-    _optional(k_gain, "k_gain", torch.bfloat16, (D,), dev)
-    x = RopeInputs(_ptr(q_gain), _ptr(k_gain), _ptr(pos))
-    if pos is not None:
-        n = 1 if axes is None else axes.n_axes
-        if axes is not None and len(axes.pairs) != D // 2:
-            raise ValueError("axes cover %d rotation pairs, D = %d has %d" %
-                             (len(axes.pairs), D, D // 2))
-        _need(pos, "pos", torch.int32)
-        shapes = [(n, B, T)] + ([(n, B)] if T == 1 else []) + ([(B, T)] if n == 1 else [])
-        if tuple(pos.shape) not in shapes:
-            raise ValueError("pos must be [n_axes, B, T] = %s, got %s" %
-                             ((n, B, T), tuple(pos.shape)))
-        if pos.device != dev:
-            raise ValueError("pos is on %s, expected %s" % (pos.device, dev))
-        x.n_axes = n
-        if axes is not None:
-            x.pair_axis = axes._array
+    gain = (D,)
+    return ("q_gain", q_gain, torch.bfloat16, gain, "k_gain", k_gain, torch.bfloat16, gain,
+            "pos", pos, torch.int32,
+            None if pos is None else _pos_shape(pos, axes, B, T, D))
+
+
+_ONE_AXIS = bytes(RopeInputs(n_axes=1))
+
+
+def _rope_inputs(q_gain, k_gain, pos, axes):
+    """The gqa_rope_inputs of these pointers, or None where nothing of it is used."""
+    if not (q_gain or k_gain or pos):
+        return None
+    x = RopeInputs.from_buffer_copy(_ONE_AXIS if axes is None else axes._inputs)
+    x.q_gain, x.k_gain, x.pos = q_gain, k_gain, pos
     return x
 
 
+@functools.lru_cache(maxsize=64)
+def _plain_params(qk_norm, eps, rope_base):
+    return RopeParams(1 if qk_norm else 0, float(eps), float(rope_base))
+
+
 def _params(qk_norm, eps, rope_base, scaling=None):
-    if scaling is None:
-        return RopeParams(1 if qk_norm else 0, float(eps), float(rope_base))
+    if scaling is None:                # passed by value: calls share the structure
+        return _plain_params(qk_norm, eps, rope_base)
     return RopeParams(1 if qk_norm else 0, float(eps), float(rope_base), ROPE_KINDS[scaling.kind],
                       scaling.factor, scaling.original_max_pos, scaling.alpha, scaling.beta)
 
@@ -557,42 +610,41 @@ def gqa_decode_noalloc(q, k_cache, v_cache, lens, max_len, out=None, scale=0.0, 
     return out
 
 
-def _append_shapes(q, k, v, cache_shape):
-    """(B, T, Hq, Hkv, D, device) of an append's new tokens; q may be None, T may be
-    left out of the shapes (the decode layout)."""
-    _need(k, "k", torch.bfloat16)
-    if k.dim() not in (3, 4):
-        raise ValueError("k must be [B, T, Hkv, D] or [B, Hkv, D], got %s" % (tuple(k.shape),))
-    B, Hkv, D = k.shape[0], k.shape[-2], k.shape[-1]
-    T = k.shape[1] if k.dim() == 4 else 1
-    _exact(v, "v", torch.bfloat16, k.shape, k.device)
-    Hq = 0
-    if q is not None:
-        _need(q, "q", torch.bfloat16, k.dim())
-        Hq = q.shape[-2]
-        _exact(q, "q", torch.bfloat16, k.shape[:-2] + (Hq, D), k.device)
-    if cache_shape[:2] != (B, Hkv) or cache_shape[3] != D:
-        raise ValueError("the cache's shape %s disagrees with k" % (tuple(cache_shape),))
-    return B, T, Hq, Hkv, D, k.device
-
-
-def _norm_rope_append(name, q, k, v, caches, cache_shape, pos0, n_tok, max_pos0, new_len, q_out,
-                      q_gain, k_gain, pos, axes, qk_norm, eps, rope_base, scaling, status, stream):
-    B, T, Hq, Hkv, D, dev = _append_shapes(q, k, v, cache_shape)
-    for what, t in (("pos0", pos0), ("n_tok", n_tok), ("new_len", new_len)):
-        _optional(t, what, torch.int32, (B,), dev)
-    _status_word(status, dev)
-    x = _rope_inputs(B, T, D, q_gain, k_gain, pos, axes, qk_norm, dev)
-    if q is None:
-        if q_out is not None:
-            raise ValueError("q_out without q")
-    elif q_out is None:
-        q_out = _new(stream, lambda: torch.empty_like(q))
+def _norm_rope_append(name, q, k, v, cache_spec, cache_shape, pos0, n_tok, max_pos0, new_len,
+                      q_out, q_gain, k_gain, pos, axes, qk_norm, eps, rope_base, scaling, status,
+                      stream):
+    _need_tensor(k, "k")
+    ks = k.shape
+    if len(ks) == 4:
+        B, T, Hkv, D = ks
+    elif len(ks) == 3:                     # decode layout [B, H, D]
+        B, Hkv, D = ks
+        T = 1
     else:
-        _exact(q_out, "q_out", torch.bfloat16, q.shape, dev)
-    _launch(name, dev, stream, _ptr(q), _ptr(k), _ptr(v), _ptr(q_out), *caches, _ptr(pos0),
-            _ptr(n_tok), int(max_pos0), _ptr(new_len), B, T, Hq, Hkv, D, cache_shape[2],
-            _params(qk_norm, eps, rope_base, scaling), x, _ptr(status))
+        raise ValueError("k must be [B, T, Hkv, D] or [B, Hkv, D], got %s" % (tuple(ks),))
+    if cache_shape[0] != B or cache_shape[1] != Hkv or cache_shape[3] != D:
+        raise ValueError("the cache's shape %s disagrees with k" % (tuple(cache_shape),))
+    Hq, qs = 0, None
+    if q is not None:
+        _need_tensor(q, "q")
+        if q.dim() != len(ks):
+            raise ValueError("q and k must have the same number of dims")
+        Hq = q.shape[-2]
+        qs = (B, T, Hq, D) if len(ks) == 4 else (B, Hq, D)
+        if q_out is None:
+            q_out = _new(stream, lambda: torch.empty_like(q))
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    bf, i32, each = torch.bfloat16, torch.int32, (B,)
+    dev = k.device
+    p = _pointers(dev, ("k", k, bf, ks, "v", v, bf, ks, "q", q, bf, qs, "q_out", q_out, bf, qs,
+                        "pos0", pos0, i32, each, "n_tok", n_tok, i32, each,
+                        "new_len", new_len, i32, each, "status", status, i32, None) +
+                  _rope_spec(B, T, D, q_gain, k_gain, pos, axes, qk_norm) + cache_spec)
+    _launch(name, dev, stream, p[-1], p[2], p[0], p[1], p[3], *p[11:-1], p[4], p[5],
+            int(max_pos0), p[6], B, T, Hq, Hkv, D, cache_shape[2],
+            _params(qk_norm, eps, rope_base, scaling), _rope_inputs(p[8], p[9], p[10], axes),
+            p[7])
     return q_out
 
 
@@ -604,13 +656,15 @@ def gqa_norm_rope_append(q, k, v, k_cache, v_cache, pos0=None, n_tok=None, max_p
     axes a RopeAxes; default pos0[b] + t) and the append of k, v, in one launch.  q, k, v
     [B, T, H, D] or [B, H, D]; q may be None.  Tokens t >= n_tok[b] are left out.
     Returns q_out (a new tensor unless given; it may be q)."""
-    _need(k_cache, "k_cache", torch.bfloat16, 4)
-    _exact(v_cache, "v_cache", torch.bfloat16, k_cache.shape, k_cache.device)
-    if isinstance(k, torch.Tensor) and k.device != k_cache.device:
-        raise ValueError("k_cache is on %s, expected %s" % (k_cache.device, k.device))
-    return _norm_rope_append("gqa_norm_rope_append", q, k, v, (_ptr(k_cache), _ptr(v_cache)),
-                             k_cache.shape, pos0, n_tok, max_pos0, new_len, q_out, q_gain, k_gain,
-                             pos, axes, qk_norm, eps, rope_base, scaling, status, stream)
+    _need_tensor(k_cache, "k_cache")
+    cs = k_cache.shape
+    if len(cs) != 4:
+        raise ValueError("k_cache must be [B, Hkv, Lmax, D], got %s" % (tuple(cs),))
+    return _norm_rope_append("gqa_norm_rope_append", q, k, v,
+                             ("k_cache", k_cache, torch.bfloat16, cs,
+                              "v_cache", v_cache, torch.bfloat16, cs), cs,
+                             pos0, n_tok, max_pos0, new_len, q_out, q_gain, k_gain, pos, axes,
+                             qk_norm, eps, rope_base, scaling, status, stream)
 
 
 def gqa_norm_rope_append_q4(q, k, v, cache, pos0=None, n_tok=None, max_pos0=-1, new_len=None,
@@ -619,9 +673,7 @@ def gqa_norm_rope_append_q4(q, k, v, cache, pos0=None, n_tok=None, max_pos0=-1, 
                             stream=None):
     """gqa_norm_rope_append into a 4-bit cache (a Q4Cache)."""
     _need_q4(cache)
-    if isinstance(k, torch.Tensor) and k.device != cache.device:
-        raise ValueError("the cache is on %s, expected %s" % (cache.device, k.device))
-    return _norm_rope_append("gqa_norm_rope_append_q4", q, k, v, cache._ptrs(), cache.shape, pos0,
+    return _norm_rope_append("gqa_norm_rope_append_q4", q, k, v, cache._spec(), cache.shape, pos0,
                              n_tok, max_pos0, new_len, q_out, q_gain, k_gain, pos, axes, qk_norm,
                              eps, rope_base, scaling, status, stream)
 
@@ -650,41 +702,40 @@ def gqa_norm_rope_append_backward(q, k, dq_out, dk_cache, dv_cache, pos0=None, m
     dq_out [B, T, Hq, D] and dk_cache, dv_cache [B, Hkv, Lmax, D] those of its outputs
     (slots pos0[b] .. pos0[b] + T - 1 are read).  dq_gain, dk_gain are float32 [D], or
     None without qk_norm."""
-    _need(q, "q", torch.bfloat16, 4)
-    dev = q.device
-    B, T, Hq, D = q.shape
-    _need(k, "k", torch.bfloat16, 4)
-    Hkv = k.shape[2]
-    _exact(k, "k", torch.bfloat16, (B, T, Hkv, D), dev)
-    _exact(dq_out, "dq_out", torch.bfloat16, q.shape, dev)
-    _need(dk_cache, "dk_cache", torch.bfloat16, 4)
-    Lmax = dk_cache.shape[2]
-    _exact(dk_cache, "dk_cache", torch.bfloat16, (B, Hkv, Lmax, D), dev)
-    _exact(dv_cache, "dv_cache", torch.bfloat16, (B, Hkv, Lmax, D), dev)
-    _optional(pos0, "pos0", torch.int32, (B,), dev)
-    _status_word(status, dev)
-    x = _rope_inputs(B, T, D, q_gain, k_gain, pos, axes, qk_norm, dev)
-    grads = [dq, dk, dv]
-    for i, (what, like) in enumerate((("dq", q), ("dk", k), ("dv", k))):
-        if grads[i] is None:
-            grads[i] = _new(stream, lambda: torch.empty_like(like))
-        else:
-            _exact(grads[i], what, torch.bfloat16, like.shape, dev)
+    for name, t in (("q", q), ("k", k), ("dk_cache", dk_cache)):
+        _need_tensor(t, name)
+        if t.dim() != 4:
+            raise ValueError("%s must have 4 dims, got %s" % (name, tuple(t.shape)))
+    qs = q.shape
+    B, T, Hq, D = qs
+    Hkv, Lmax, dev = k.shape[2], dk_cache.shape[2], q.device
+    ks, cs = (B, T, Hkv, D), (B, Hkv, Lmax, D)
+    if dq_out is None or dv_cache is None:
+        raise TypeError("dq_out and dv_cache must be tensors")
+    dq = _new(stream, lambda: torch.empty_like(q)) if dq is None else dq
+    dk = _new(stream, lambda: torch.empty_like(k)) if dk is None else dk
+    dv = _new(stream, lambda: torch.empty_like(k)) if dv is None else dv
+    bf = torch.bfloat16
+    rope = _rope_spec(B, T, D, q_gain, k_gain, pos, axes, qk_norm)
     dg, ws_bytes = (None, None), 0
-    if qk_norm:
+    if qk_norm and dev.type == "cuda":
         dg = _new(stream, lambda: torch.empty(2, D, dtype=torch.float32, device=dev)).unbind(0)
         if workspace is None:
             workspace = _new(stream, lambda: norm_rope_backward_workspace(D, dev))
-        _need(workspace, "workspace", torch.uint8)
-        if workspace.device != dev:
-            raise ValueError("workspace is on %s, expected %s" % (workspace.device, dev))
+        _need_tensor(workspace, "workspace")
         ws_bytes = workspace.numel()
-    _launch("gqa_norm_rope_append_backward", dev, stream, _ptr(q), _ptr(k), _ptr(dq_out),
-            _ptr(dk_cache), _ptr(dv_cache), _ptr(grads[0]), _ptr(grads[1]), _ptr(grads[2]),
-            _ptr(dg[0]), _ptr(dg[1]), _ptr(pos0), int(max_pos0), B, T, Hq, Hkv, D, Lmax,
-            _params(qk_norm, eps, rope_base, scaling), x, _ptr(workspace), ws_bytes,
-            _ptr(status))
-    return grads[0], grads[1], grads[2], dg[0], dg[1]
+    p = _pointers(dev, ("q", q, bf, qs, "k", k, bf, ks, "dq_out", dq_out, bf, qs,
+                        "dk_cache", dk_cache, bf, cs, "dv_cache", dv_cache, bf, cs,
+                        "dq", dq, bf, qs, "dk", dk, bf, ks, "dv", dv, bf, ks,
+                        "dq_gain", dg[0], torch.float32, (D,),
+                        "dk_gain", dg[1], torch.float32, (D,),
+                        "pos0", pos0, torch.int32, (B,),
+                        "workspace", workspace, torch.uint8, None,
+                        "status", status, torch.int32, None) + rope)
+    _launch("gqa_norm_rope_append_backward", dev, stream, p[-1], *p[:11], int(max_pos0), B, T, Hq,
+            Hkv, D, Lmax, _params(qk_norm, eps, rope_base, scaling),
+            _rope_inputs(p[13], p[14], p[15], axes), p[11], ws_bytes, p[12])
+    return dq, dk, dv, dg[0], dg[1]
 
 
 def kv_cache_read_q4(cache, k_out=None, v_out=None, first=None, count=None, status=None,
@@ -695,20 +746,20 @@ def kv_cache_read_q4(cache, k_out=None, v_out=None, first=None, count=None, stat
     _need_q4(cache)
     B, Hkv, Lmax, D = cache.shape
     dev = cache.device
-    for what, t in (("first", first), ("count", count)):
-        _optional(t, what, torch.int32, (B,), dev)
-    _status_word(status, dev)
     if (k_out is None) != (v_out is None):
         raise ValueError("k_out and v_out go together")
     if k_out is None:
         k_out, v_out = (_new(stream, lambda: torch.zeros(B, Hkv, Lmax, D, dtype=torch.bfloat16,
                                                          device=dev)) for _ in range(2))
-    _need(k_out, "k_out", torch.bfloat16, 4)
+    _need_tensor(k_out, "k_out")
+    if k_out.dim() != 4:
+        raise ValueError("k_out must be [B, Hkv, Lout, D], got %s" % (tuple(k_out.shape),))
     Lout = k_out.shape[2]
-    _exact(k_out, "k_out", torch.bfloat16, (B, Hkv, Lout, D), dev)
-    _exact(v_out, "v_out", torch.bfloat16, (B, Hkv, Lout, D), dev)
-    _launch("kv_cache_read_q4", dev, stream, *cache._ptrs(), _ptr(first), _ptr(count),
-            _ptr(k_out), _ptr(v_out), B, Hkv, D, Lmax, Lout, _ptr(status))
+    shape, bf, i32 = (B, Hkv, Lout, D), torch.bfloat16, torch.int32
+    p = _pointers(dev, cache._spec() + ("first", first, i32, (B,), "count", count, i32, (B,),
+                                        "k_out", k_out, bf, shape, "v_out", v_out, bf, shape,
+                                        "status", status, i32, None))
+    _launch("kv_cache_read_q4", dev, stream, p[-1], *p[:8], B, Hkv, D, Lmax, Lout, p[8])
     return k_out, v_out
 
 
@@ -728,22 +779,24 @@ def gqa_decode_q4(q, cache, lens, max_len, out=None, workspace=None, scale=0.0, 
     """One query token per sequence against a 4-bit cache: q [B, Hq, D], lens[b] cached
     tokens of a Q4Cache, the new one included."""
     _need_q4(cache)
+    _need_tensor(q, "q")
+    _need_tensor(lens, "lens")
     B, Hkv, Lmax, D = cache.shape
     dev = cache.device
-    _need(q, "q", torch.bfloat16, 3)
+    if q.dim() != 3:
+        raise ValueError("q must be [B, Hq, D], got %s" % (tuple(q.shape),))
     Hq = q.shape[1]
-    _exact(q, "q", torch.bfloat16, (B, Hq, D), dev)
-    _exact(lens, "lens", torch.int32, (B,), dev)
-    _status_word(status, dev)
+    shape = (B, Hq, D)
     if out is None:
         out = _new(stream, lambda: torch.empty_like(q))
-    _exact(out, "out", torch.bfloat16, q.shape, dev)
     if workspace is None:
         workspace = _new(stream, lambda: decode_q4_workspace(B, Hq, Hkv, D, max_len, dev))
-    _need(workspace, "workspace", torch.uint8)
-    if workspace.device != dev:
-        raise ValueError("workspace is on %s, expected %s" % (workspace.device, dev))
-    _launch("gqa_decode_q4", dev, stream, _ptr(q), *cache._ptrs(), _ptr(lens), int(max_len),
-            _ptr(out), B, Hq, Hkv, D, Lmax, float(scale), _ptr(workspace), workspace.numel(),
-            _ptr(status))
+    _need_tensor(workspace, "workspace")
+    bf = torch.bfloat16
+    p = _pointers(dev, ("q", q, bf, shape) + cache._spec() +
+                  ("lens", lens, torch.int32, (B,), "out", out, bf, shape,
+                   "workspace", workspace, torch.uint8, None,
+                   "status", status, torch.int32, None))
+    _launch("gqa_decode_q4", dev, stream, p[-1], *p[:6], int(max_len), p[6], B, Hq, Hkv, D, Lmax,
+            float(scale), p[7], workspace.numel(), p[8])
     return out

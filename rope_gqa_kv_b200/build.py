@@ -5,6 +5,8 @@
 Each .cu is compiled to an object in _build/ (parallel), then linked into
 rope_gqa_kv_b200/libgqa.so with the CUDA runtime linked statically.  A source
 is rebuilt when it, or any header it may include, is newer than its object.
+csrc/fastargs.c, the argument checks of the Python binding, becomes the extension
+module rope_gqa_kv_b200/_fastargs.so (gcc).
 """
 from __future__ import annotations
 
@@ -15,12 +17,15 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OBJ_DIR = os.path.join(ROOT, "_build", "gqa")
 LIB = os.path.join(PKG, "libgqa.so")
+ARGS_SRC = os.path.join(CSRC, "fastargs.c")
+ARGS_LIB = os.path.join(PKG, "_fastargs.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
@@ -52,8 +57,24 @@ def _compile(src: str, verbose: bool) -> tuple[str, str]:
     return obj, r.stderr
 
 
+def _build_args(force: bool) -> None:
+    if not force and os.path.exists(ARGS_LIB) and \
+            os.path.getmtime(ARGS_LIB) >= os.path.getmtime(ARGS_SRC):
+        return
+    import torch
+    tmp = ARGS_LIB + ".tmp%d" % os.getpid()
+    cmd = [shutil.which("gcc") or "gcc", "-O2", "-Wall", "-shared", "-fPIC",
+           "-I", sysconfig.get_paths()["include"],
+           "-I", os.path.join(os.path.dirname(torch.__file__), "include"), ARGS_SRC, "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("gcc failed:\n%s\n%s" % (" ".join(cmd), r.stderr))
+    os.replace(tmp, ARGS_LIB)
+
+
 def build(force: bool = False, verbose: bool = False, jobs: int = 0) -> str:
     os.makedirs(OBJ_DIR, exist_ok=True)
+    _build_args(force)
     srcs = _sources()
     newest_hdr = max((os.path.getmtime(h) for h in _headers()), default=0.0)
     todo = []

@@ -9,30 +9,34 @@
 // codes per clock, three query heads make that 135 multiply-adds per clock, and
 // each code has to be unpacked first; scalar arithmetic cannot keep up, so the
 // products run on the tensor cores with the codes as they are:
-//   * (w & 0x000f000f) | 0x43004300 turns two codes of a word into the bf16 pair
-//     128 + c, exactly, in one instruction.  Codes are the 16-row operand of
-//     mma.m16n8k16 (rows = keys for the scores, coordinates for the output) and the
-//     query heads its 8 columns: a group of heads costs what one head costs.
-//   * scores: q is bf16 already, so the products are exact; a group's sum a is
-//     scaled and shifted once: s a + (m - 128 s) sum(q) over the group.
-//   * output: sum_k p_k (m_k + s_k c_k,d).  p_k s_k goes in as the 8-column operand,
-//     carried by movmatrix from the score layout.  Rounded to bf16 it would cost
-//     2^-9 per term, so it goes in twice, as a rounded part and the bf16 of what the
-//     rounding left (2^-17 together): with up to 4 heads per CTA the second part
-//     uses columns 4 .. 7 (q is repeated there, so those lanes hold the same p),
-//     with 5 .. 8 a second mma.  The 128 in every code is taken out by a column sum
-//     of the same operand, 128 sum(p s), from one more mma; sum(p m) is added up in
-//     fp32 beside it.
+//   * a 4-bit number in the low bits of a 16-bit float is a subnormal: c stands for
+//     c 2^-133 in bf16 and c 2^-24 in fp16, and four bits higher for 16 times that,
+//     all exact in the product.  One AND of a word of codes so gives two of them
+//     (code_pair); a word's eight codes take five instructions.  Codes are the
+//     16-row operand of mma.m16n8k16 (rows = keys for the scores, coordinates for the
+//     output) and the query heads its 8 columns: a group of heads costs what one
+//     head costs.
+//   * scores: q stays bf16, times 2^64 (2^60 against the codes four bits up), so the
+//     products are exact; a key's s multiplies the sum of its group.  The minima's
+//     part, sum over groups of m sum(q), is one more product whose 16-row operand is
+//     the (s, m) words themselves, with sum(q) in three bf16 parts (24 bits).
+//   * output: sum_k p_k (m_k + s_k c_k,d).  p_k s_k is the 8-column operand, carried
+//     by movmatrix from the score layout, in fp16 after a power of two that brings the
+//     largest s so far to 2^5 .. 2^6: one rounding, 2^-12 of the term, against bf16's
+//     2^-9 (terms below 2^-20 of the largest lose bits, 2^-31 of it at most).
+//     sum(p m) is added up in fp32 beside it.
 // mma.sync rather than tcgen05: its operands come from registers, where the codes
 // are unpacked; tcgen05 would need them written to shared memory as bf16, four
 // times the bytes that arrived, for 8 columns of work.
 //
-// Work: as decode.cu, one CTA per (chunk of 64 NT cache slots, KV head x head
-// subgroup, sequence), its loads four bulk copies (K codes and scales with q on one
-// barrier, V's on another), its four warps taking 16-key tiles in turn; statistics
-// and partial outputs are merged in shared memory, the chunk's (m, l, o) goes to
-// the workspace and a second kernel, a programmatic dependent, merges the chunks.
-// When one chunk covers max_len the CTA writes the output itself.
+// Work: one CTA per (chunk of the cached slots, KV head x head subgroup, sequence).
+// Its four warps take the chunk's 16-key tiles in turn, each through a ring of its own
+// (asynchronous 16-byte copies, kStages tiles deep; no warp waits for another), with a
+// running softmax: the reference moves, and what is summed is scaled down, only when a
+// score passes it by more than 8, i.e. hardly ever after the first tile.  At the end
+// the warps' statistics and partial outputs are merged in shared memory, the chunk's
+// (m, l, o) goes to the workspace and a second kernel, a programmatic dependent,
+// merges the chunks.  When one chunk covers max_len the CTA writes the output itself.
 #include "q4.cuh"
 #include "ptx.cuh"
 #include "rope.cuh"
@@ -43,11 +47,23 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kCols = 8;               // columns of the mma: query heads of a CTA, at most
+constexpr int kStages = 4;             // tiles of a warp's ring
+constexpr float kSlack = 8.0f;         // a score may pass the softmax reference by this
+constexpr float kNoRef = -1e30f;       // the reference before any score: finite, so that
+                                       // 2^(a score of -inf - it) is 0
 
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
+        "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
         "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -60,10 +76,26 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t a) {
     return d;
 }
 
-// Codes at bits 0 and 16 of w >> sh as the bf16 pair 128 + c.
-__device__ __forceinline__ uint32_t code_pair(uint32_t w, int sh) {
-    return ((w >> sh) & 0x000f000fu) | 0x43004300u;
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
 }
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    uint32_t d;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+
+// Two codes of a word as subnormal numbers: those in the low four bits of each half,
+// and the ones above them (16 times as large).
+__device__ __forceinline__ uint32_t code_pair(uint32_t w) { return w & 0x000f000fu; }
+__device__ __forceinline__ uint32_t code_pair16(uint32_t w) { return w & 0x00f000f0u; }
 
 template <int NG>
 __device__ __forceinline__ void load_words(uint32_t (&w)[NG], const uint32_t *p) {
@@ -79,27 +111,34 @@ __device__ __forceinline__ void load_words(uint32_t (&w)[NG], const uint32_t *p)
     }
 }
 
-template <int D, int NT>
+// 16 bytes, global to shared, the last 16 - n of them zeros; counted by commit groups.
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, int n = 16) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
+                 : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+template <int D>
 struct DecQ4Shape {
     static constexpr int NG = Q4Shape<D>::NG;
-    static constexpr int CH = 64 * NT;                     // cache slots per CTA
-    static constexpr int kRowWords = D / 8;                // 4-byte words of codes per row
-    static constexpr int kCode = CH * D / 2;
-    static constexpr int kScale = CH * 4 * NG;
-    // [K codes][K scales][V codes][V scales] | [q][(m, l)]; the warps' partial
-    // outputs (kWarps x kCols x (D + 4) f32) are written over the first part once
-    // every warp is done with it.  D + 4: the four lanes of a row write four columns,
-    // 8 banks apart.
-    static constexpr int kOffKS = kCode;
-    static constexpr int kOffV = kCode + kScale;
-    static constexpr int kOffVS = kOffV + kCode;
+    static constexpr int RB = D / 2;                       // bytes of codes per row
+    static constexpr int SB = 4 * NG;                      // bytes of scales per row
+    // A tile in the ring: [K codes][V codes][K scales][V scales], 16 rows each.
+    static constexpr int kOffV = 16 * RB;
+    static constexpr int kOffKS = 32 * RB;
+    static constexpr int kOffVS = 32 * RB + 16 * SB;
+    static constexpr int kTile = 32 * (RB + SB);
+    static constexpr int kRing = kWarps * kStages * kTile;
+    // The warps' partial outputs (kWarps x kCols x (D + 4) f32) are written over the
+    // rings once every warp is done.  D + 4: the four lanes of a row write four
+    // columns, 8 banks apart.
     static constexpr int kPartStride = D + 4;
     static constexpr int kPart = kWarps * kCols * kPartStride * 4;
-    static constexpr int kData = kOffVS + kScale;
-    static constexpr int kOffQ = (kData > kPart ? kData : kPart) + 0;
-    static constexpr int kOffML = kOffQ + kCols * D * 2;
-    static constexpr int kSmem = kOffML + kWarps * kCols * 2 * 4;
-    static_assert(kOffQ % 16 == 0 && kOffV % 16 == 0 && kOffVS % 16 == 0, "alignment");
+    static constexpr int kSmem = kRing > kPart ? kRing : kPart;
 };
 
 struct DecQ4Args {
@@ -110,19 +149,20 @@ struct DecQ4Args {
     uint16_t *out;
     float *ws_ml, *ws_o;
     int32_t *status;
-    int max_len, B, Hq, Hkv, Lmax, n_splits, n_sub, G;   // G: query heads per CTA
-    float scale_log2;
+    int max_len, B, Hq, Hkv, Lmax, n_sub, G;               // G: query heads per CTA
+    int chunk, n_splits;                                   // slots per CTA, chunks of max_len
+    float scale_log2;                  // 2^69 scale / ln 2: the scores come in units of 2^-69
 };
 
 // Workspace: [(m, l): rows x 2 f32][o: rows x D f32], rows = B x Hq x n_splits, row
-// (b, h, c) = (b * Hq + h) * n_splits + c.  WIDE: 5 .. 8 query heads per CTA.
-template <int D, int NT, bool WIDE>
+// (b, h, c) = (b * Hq + h) * n_splits + c.
+template <int D>
 __global__ void __launch_bounds__(kThreads, 4)
 decode_q4_kernel(const DecQ4Args A) {
-    using S = DecQ4Shape<D, NT>;
+    using S = DecQ4Shape<D>;
     constexpr int NG = S::NG;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ __align__(8) uint64_t bars[2];              // [0]: K and q, [1]: V
+    __shared__ float wml[kWarps * kCols * 2];              // (m, l) [warp][column]
     __shared__ float sw[kWarps * kCols];                   // merge weights [warp][column]
     __shared__ float s_inv[kCols];
 
@@ -145,209 +185,265 @@ decode_q4_kernel(const DecQ4Args A) {
             for (int i = tid; i < G * D; i += kThreads) A.out[((size_t)b * A.Hq + h0) * D + i] = 0;
         return;
     }
-    const int key0 = c * S::CH;
+    const int key0 = c * A.chunk;
     if (key0 >= len) return;
-    const int nk = min(S::CH, len - key0);
-    const uint32_t bar_k = ptx::smem_addr(&bars[0]);
-    const uint32_t bar_v = ptx::smem_addr(&bars[1]);
-    if (tid == 0) {
-        ptx::mbar_init(bar_k, 1);
-        ptx::mbar_init(bar_v, 1);
-        ptx::fence_barrier_init();
-        // Whole groups of 4 rows: a row's scales may be 8 or 12 bytes and a bulk copy
-        // moves multiples of 16.  Lmax is a multiple of 128, so the rows exist.
-        const int nr = (nk + 3) & ~3;
-        const uint32_t cb = (uint32_t)nr * (D / 2), sb = (uint32_t)nr * (4 * NG);
-        const size_t row = ((size_t)b * A.Hkv + kvh) * A.Lmax + key0;
-        const uint64_t pol = ptx::policy_evict_first();
-        ptx::mbar_arrive_expect_tx(bar_k, cb + sb + G * D * 2);
-        ptx::bulk_g2s(ptx::smem_addr(smem + S::kOffQ), A.q + ((size_t)b * A.Hq + h0) * D,
-                      G * D * 2, bar_k);
-        ptx::bulk_g2s_hint(ptx::smem_addr(smem), A.kc + row * (D / 2), cb, bar_k, pol);
-        ptx::bulk_g2s_hint(ptx::smem_addr(smem + S::kOffKS), A.ks + row * NG, sb, bar_k, pol);
-        ptx::mbar_arrive_expect_tx(bar_v, cb + sb);
-        ptx::bulk_g2s_hint(ptx::smem_addr(smem + S::kOffV), A.vc + row * (D / 2), cb, bar_v, pol);
-        ptx::bulk_g2s_hint(ptx::smem_addr(smem + S::kOffVS), A.vs + row * NG, sb, bar_v, pol);
-    }
-    __syncthreads();                   // barriers initialised before anyone waits on them
-    const uint32_t *kw = reinterpret_cast<const uint32_t *>(smem);
-    const uint32_t *ksw = reinterpret_cast<const uint32_t *>(smem + S::kOffKS);
-    const uint32_t *vw = reinterpret_cast<const uint32_t *>(smem + S::kOffV);
-    const uint32_t *vsw = reinterpret_cast<const uint32_t *>(smem + S::kOffVS);
-    const uint16_t *qs = reinterpret_cast<const uint16_t *>(smem + S::kOffQ);
-    float *wml = reinterpret_cast<float *>(smem + S::kOffML);        // [warp][column][2]
-    float *part = reinterpret_cast<float *>(smem);                   // [warp][column][D + 4]
-    if (!__syncthreads_and(ptx::mbar_wait(bar_k, 0))) {
-        // A late copy may still land in this CTA's shared memory: one more bounded
-        // wait for both before the CTA retires.
-        ptx::mbar_wait(bar_k, 0);
-        ptx::mbar_wait(bar_v, 0);
-        if (tid == 0) report(A.status, GQA_DEV_TIMEOUT);
-        return;
+    const int nk = min(A.chunk, len - key0);
+
+    // ---- the warp's ring ----
+    // A lane copies 16 bytes of each 512-byte block of codes, and 16 of the scales:
+    // lanes 0 .. 15 K's, lanes 16 .. 31 V's.
+    const size_t row = ((size_t)b * A.Hkv + kvh) * A.Lmax + key0;
+    const uint8_t *kg = A.kc + row * S::RB + 16 * lane, *vg = A.vc + row * S::RB + 16 * lane;
+    const uint8_t *sg = reinterpret_cast<const uint8_t *>(lane < 16 ? A.ks : A.vs) +
+                        row * S::SB + 16 * (lane & 15);
+    const uint32_t ring = ptx::smem_addr(smem) + warp * (kStages * S::kTile) + 16 * lane;
+    const uint32_t ring_s = ring + S::kOffKS + (lane < 16 ? 0 : 16 * S::SB - 256);
+    const int n_tiles = (nk + 15) >> 4;
+    // Tile t (keys 16 t ..) to a stage.  The rows behind the length are not read: their
+    // codes and scales are zeros.
+    auto fetch = [&](int t, int stage) {
+        const uint8_t *k = kg + (size_t)t * (16 * S::RB), *v = vg + (size_t)t * (16 * S::RB);
+        const uint8_t *s = sg + (size_t)t * (16 * S::SB);
+        const uint32_t dst = ring + stage * S::kTile, dst_s = ring_s + stage * S::kTile;
+        if (16 * t + 16 <= nk) {                           // uniform across the warp
+#pragma unroll
+            for (int x = 0; x < 16 * S::RB; x += 512)
+                if (x + 512 <= 16 * S::RB || x + 16 * lane < 16 * S::RB) {
+                    copy16(dst + x, k + x);
+                    copy16(dst + S::kOffV + x, v + x);
+                }
+            if ((lane & 15) < S::SB) copy16(dst_s, s);
+        } else {
+            const int live = nk - 16 * t;
+#pragma unroll
+            for (int x = 0; x < 16 * S::RB; x += 512)
+                if (x + 512 <= 16 * S::RB || x + 16 * lane < 16 * S::RB) {
+                    const int n = min(16, max(0, live * S::RB - x - 16 * lane));
+                    copy16(dst + x, k + x, n);
+                    copy16(dst + S::kOffV + x, v + x, n);
+                }
+            if ((lane & 15) < S::SB)
+                copy16(dst_s, s, min(16, max(0, live * S::SB - 16 * (lane & 15))));
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) {
+        if (warp + kWarps * i < n_tiles) fetch(warp + kWarps * i, i);
+        copy_commit();
     }
 
     const int r = lane >> 2, kk = lane & 3;
-    // q as the 8-column operand: column r is head r (WIDE) or r & 3.  Word kk of group
-    // g covers coordinates 16 g + 4 kk .. + 3 and their partners in the second half;
-    // code_pair(w, 0), (w, 4), (w, 8), (w, 12) are coordinates (0, 2) of the first
-    // half, of the second, (1, 3) of the first, of the second.
+    // Row r of a product's first eight is key sr of the tile, row r + 8 key sr + 8: any
+    // order serves, and with this one the four rows that a load of V touches are
+    // neighbours, which fall into different banks.
+    const int sr = (r >> 1) + 4 * (r & 1);
+    // q as the 8-column operand: column r is head r.  Word kk of group g covers
+    // coordinates 16 g + 4 kk .. + 3 and their partners in the second half; its codes
+    // come as coordinates (0, 2) of the first half, of the second (times 16), and,
+    // shifted down by 8, (1, 3) of the first, of the second (times 16).
     uint32_t bq[NG][4];
-    float qsum[NG][2];                 // sum of q over the group, heads of columns 2kk, 2kk+1
+    uint32_t bm[3];                    // sum of q over group kk, head r: bf16 parts, high half
     {
-        const int hr = WIDE ? r : (r & 3);
+        const uint16_t *q = A.q + ((size_t)b * A.Hq + h0 + r) * D + 4 * kk;
+        uint2 lo[NG], hi[NG];
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
-            uint2 lo = make_uint2(0, 0), hi = make_uint2(0, 0);
-            if (hr < G) {
-                lo = *reinterpret_cast<const uint2 *>(qs + hr * D + 16 * g + 4 * kk);
-                hi = *reinterpret_cast<const uint2 *>(qs + hr * D + D / 2 + 16 * g + 4 * kk);
+            lo[g] = hi[g] = make_uint2(0, 0);
+            if (r < G) {
+                lo[g] = *reinterpret_cast<const uint2 *>(q + 16 * g);
+                hi[g] = *reinterpret_cast<const uint2 *>(q + D / 2 + 16 * g);
             }
-            bq[g][0] = __byte_perm(lo.x, lo.y, 0x5410);
-            bq[g][1] = __byte_perm(hi.x, hi.y, 0x5410);
-            bq[g][2] = __byte_perm(lo.x, lo.y, 0x7632);
-            bq[g][3] = __byte_perm(hi.x, hi.y, 0x7632);
+        }
+        float qsum[8];                 // [2 g + e]: heads of columns 2 kk + e
+#pragma unroll
+        for (int i = 0; i < 8; ++i) qsum[i] = 0.f;
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            bq[g][0] = __byte_perm(lo[g].x, lo[g].y, 0x5410);
+            bq[g][1] = __byte_perm(hi[g].x, hi[g].y, 0x5410);
+            bq[g][2] = __byte_perm(lo[g].x, lo[g].y, 0x7632);
+            bq[g][3] = __byte_perm(hi[g].x, hi[g].y, 0x7632);
             float acc[4] = {0.f, 0.f, 0.f, 0.f};
             constexpr uint32_t one = 0x3f803f80u;
             mma_bf16(acc, one, one, one, one, bq[g][0], bq[g][1]);
             mma_bf16(acc, one, one, one, one, bq[g][2], bq[g][3]);
-            qsum[g][0] = acc[0];
-            qsum[g][1] = acc[1];
+            qsum[2 * g] = acc[0];
+            qsum[2 * g + 1] = acc[1];
+            constexpr uint32_t up64 = 0x5f805f80u, up60 = 0x5d805d80u;   // 2^64, 2^60 twice
+            bq[g][0] = mul_bf16x2(bq[g][0], up64);
+            bq[g][1] = mul_bf16x2(bq[g][1], up60);
+            bq[g][2] = mul_bf16x2(bq[g][2], up64);
+            bq[g][3] = mul_bf16x2(bq[g][3], up60);
+        }
+        // Every row r of the sums is alike: lane (r, k) offers group r / 2 of head
+        // 2 k + r % 2, and fetches group kk of head r.
+        float mine = qsum[0];
+#pragma unroll
+        for (int i = 1; i < 8; ++i) mine = r == i ? qsum[i] : mine;
+        float x = __shfl_sync(0xffffffffu, mine, 4 * (2 * kk + (r & 1)) + (r >> 1));
+        x *= 0x1p-69f;                 // the scores' unit: 2^64 2^-133
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+            bm[i] = pack_bf16x2(0.f, x);
+            x -= bf16hi(bm[i]);
         }
     }
 
-    // ---- scores of the warp's tiles: tile i holds keys 16 (4 i + warp) .. + 15 ----
-    // Lane (r, kk) has keys r and r + 8 of the tile against columns 2 kk, 2 kk + 1.
-    float sc[NT][4];
-#pragma unroll
-    for (int i = 0; i < NT; ++i) {
-        const int t0 = 16 * (kWarps * i + warp);
-        sc[i][0] = sc[i][1] = sc[i][2] = sc[i][3] = -INFINITY;
-        if (t0 < nk) {                                     // uniform across the warp
-            uint32_t w0[NG], w1[NG], m0[NG], m1[NG];
-            load_words<NG>(w0, kw + (t0 + r) * S::kRowWords + NG * kk);
-            load_words<NG>(w1, kw + (t0 + r + 8) * S::kRowWords + NG * kk);
-            load_words<NG>(m0, ksw + (t0 + r) * NG);
-            load_words<NG>(m1, ksw + (t0 + r + 8) * NG);
-            float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
-#pragma unroll
-            for (int g = 0; g < NG; ++g) {
-                float acc[4] = {0.f, 0.f, 0.f, 0.f};
-                mma_bf16(acc, code_pair(w0[g], 0), code_pair(w1[g], 0), code_pair(w0[g], 4),
-                         code_pair(w1[g], 4), bq[g][0], bq[g][1]);
-                mma_bf16(acc, code_pair(w0[g], 8), code_pair(w1[g], 8), code_pair(w0[g], 12),
-                         code_pair(w1[g], 12), bq[g][2], bq[g][3]);
-                const float s0 = bf16lo(m0[g]), s1 = bf16lo(m1[g]);
-                const float z0 = fmaf(-128.f, s0, bf16hi(m0[g]));
-                const float z1 = fmaf(-128.f, s1, bf16hi(m1[g]));
-                ptx::ffma2(a0, a1, s0, s0, acc[0], acc[1], a0, a1);
-                ptx::ffma2(a0, a1, z0, z0, qsum[g][0], qsum[g][1], a0, a1);
-                ptx::ffma2(a2, a3, s1, s1, acc[2], acc[3], a2, a3);
-                ptx::ffma2(a2, a3, z1, z1, qsum[g][0], qsum[g][1], a2, a3);
-            }
-            if (t0 + r < nk) {
-                sc[i][0] = a0 * A.scale_log2;
-                sc[i][1] = a1 * A.scale_log2;
-            }
-            if (t0 + r + 8 < nk) {
-                sc[i][2] = a2 * A.scale_log2;
-                sc[i][3] = a3 * A.scale_log2;
-            }
-        }
-    }
-
-    // ---- the warp's softmax statistics (base 2) per column ----
-    float mw[2], lw[2];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        float m = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < NT; ++i) m = fmaxf(m, fmaxf(sc[i][e], sc[i][e + 2]));
-#pragma unroll
-        for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const float ref = m == -INFINITY ? 0.f : m;        // a warp with no live key
-        float l = 0.f;
-#pragma unroll
-        for (int i = 0; i < NT; ++i) {
-            sc[i][e] = ex2(sc[i][e] - ref);
-            sc[i][e + 2] = ex2(sc[i][e + 2] - ref);
-            l += sc[i][e] + sc[i][e + 2];
-        }
-#pragma unroll
-        for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-        mw[e] = m;
-        lw[e] = l;
-    }
-
-    // ---- output: rows = coordinates, columns = heads ----
-    if (!__syncthreads_and(ptx::mbar_wait(bar_v, 0))) {
-        ptx::mbar_wait(bar_v, 0);
-        if (tid == 0) report(A.status, GQA_DEV_TIMEOUT);
-        return;
-    }
+    // State of the running softmax.  Lane (r, kk): columns 2 kk, 2 kk + 1; the sums of
+    // p and p m are over the lane's own rows, o over all of them.
+    float ref[2] = {kNoRef, kNoRef}, l[2] = {0.f, 0.f};
     float o[NG][2][4];                 // [g][jj]: coordinates 16 g + 2 r + jj, D/2 + the same
-    float off[NG][4];                  // 128 sum(p s), the same in every row
-    float pm[NG][2];                   // this lane's keys' share of sum(p m)
+    float pm[NG][2];
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[g][0][e] = o[g][1][e] = off[g][e] = 0.f;
+        for (int e = 0; e < 4; ++e) o[g][0][e] = o[g][1][e] = 0.f;
         pm[g][0] = pm[g][1] = 0.f;
     }
-    // Columns 4 .. 7 hold what bf16 left of columns 0 .. 3 (not WIDE).
-    const uint32_t rest = !WIDE && kk >= 2 ? 0xffffffffu : 0u;
+    // p s goes into fp16 times up = 2^(132 - eb), eb the biased exponent of the largest V
+    // step so far: p <= 2^kSlack keeps it below 2^14, and steps may double twice before
+    // the sums have to follow (cap).  o is in units of 2^(eb - 108), with the codes' 2^-24.
+    uint32_t eb = 0;
+    float up = 0.f, cap = 0.f;
     const uint32_t sel = (r & 1) ? 0x7632u : 0x5410u;
-#pragma unroll
-    for (int i = 0; i < NT; ++i) {
-        const int t0 = 16 * (kWarps * i + warp);
-        if (t0 < nk) {                                     // uniform across the warp
-            uint32_t m0[NG], m1[NG], wa[NG], wb[NG], wc[NG], wd[NG];
-            load_words<NG>(m0, vsw + (t0 + r) * NG);
-            load_words<NG>(m1, vsw + (t0 + r + 8) * NG);
-            const uint32_t *vr = vw + (t0 + 2 * kk) * S::kRowWords + NG * (r >> 1);
-            load_words<NG>(wa, vr);
-            load_words<NG>(wb, vr + S::kRowWords);
-            load_words<NG>(wc, vr + 8 * S::kRowWords);
-            load_words<NG>(wd, vr + 9 * S::kRowWords);
-            const bool live0 = t0 + r < nk, live1 = t0 + r + 8 < nk;
+
+    int stage = 0;
+#pragma unroll 1
+    for (int t = warp; t < n_tiles; t += kWarps) {
+        copy_wait<kStages - 2>();
+        __syncwarp();
+        {
+            const int ahead = t + kWarps * (kStages - 1);  // into the stage read last
+            if (ahead < n_tiles) fetch(ahead, (stage + kStages - 1) % kStages);
+            copy_commit();
+        }
+        const uint8_t *tile = smem + (warp * kStages + stage) * S::kTile;
+        stage = (stage + 1) % kStages;
+        const uint32_t *kw = reinterpret_cast<const uint32_t *>(tile);
+        const uint32_t *vw = reinterpret_cast<const uint32_t *>(tile + S::kOffV);
+        const uint32_t *ksw = reinterpret_cast<const uint32_t *>(tile + S::kOffKS);
+        const uint32_t *vsw = reinterpret_cast<const uint32_t *>(tile + S::kOffVS);
+
+        // ---- scores: lane (r, kk) has rows r and r + 8 against its two columns ----
+        float sc[4] = {0.f, 0.f, 0.f, 0.f};
+        {
+            uint32_t w0[NG], w1[NG], m0[NG], m1[NG];
+            load_words<NG>(w0, kw + sr * (S::RB / 4) + NG * kk);
+            load_words<NG>(w1, kw + (sr + 8) * (S::RB / 4) + NG * kk);
+            load_words<NG>(m0, ksw + sr * NG);
+            load_words<NG>(m1, ksw + (sr + 8) * NG);
+            const uint32_t mk0 = ksw[sr * NG + min(kk, NG - 1)];
+            const uint32_t mk1 = ksw[(sr + 8) * NG + min(kk, NG - 1)];
+            mma_bf16(sc, mk0, mk1, mk0, mk1, bm[0], bm[1]);
+            mma_bf16(sc, mk0, mk1, mk0, mk1, bm[2], 0u);
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
-                // Rows behind the length may hold anything: their scales count as 0.
-                const uint32_t x0 = live0 ? m0[g] : 0u, x1 = live1 ? m1[g] : 0u;
-                const float s0 = bf16lo(x0), s1 = bf16lo(x1);
-                ptx::ffma2(pm[g][0], pm[g][1], bf16hi(x0), bf16hi(x0), sc[i][0], sc[i][1],
-                           pm[g][0], pm[g][1]);
-                ptx::ffma2(pm[g][0], pm[g][1], bf16hi(x1), bf16hi(x1), sc[i][2], sc[i][3],
-                           pm[g][0], pm[g][1]);
-                const float p0 = sc[i][0] * s0, p1 = sc[i][1] * s0;
-                const float p2 = sc[i][2] * s1, p3 = sc[i][3] * s1;
-                uint32_t h01 = pack_bf16x2(p0, p1), h23 = pack_bf16x2(p2, p3);
-                const uint32_t y0 = __byte_perm(wa[g], wb[g], sel);
-                const uint32_t y1 = __byte_perm(wc[g], wd[g], sel);
-                const uint32_t c00 = code_pair(y0, 0), c01 = code_pair(y0, 4);
-                const uint32_t c02 = code_pair(y1, 0), c03 = code_pair(y1, 4);
-                const uint32_t c10 = code_pair(y0, 8), c11 = code_pair(y0, 12);
-                const uint32_t c12 = code_pair(y1, 8), c13 = code_pair(y1, 12);
-                constexpr uint32_t k128 = 0x43004300u;
-                if constexpr (WIDE) {
-                    const uint32_t l01 = pack_bf16x2(p0 - bf16lo(h01), p1 - bf16hi(h01));
-                    const uint32_t l23 = pack_bf16x2(p2 - bf16lo(h23), p3 - bf16hi(h23));
-                    const uint32_t b0 = transpose8(l01), b1 = transpose8(l23);
-                    mma_bf16(o[g][0], c00, c01, c02, c03, b0, b1);
-                    mma_bf16(o[g][1], c10, c11, c12, c13, b0, b1);
-                    mma_bf16(off[g], k128, k128, k128, k128, b0, b1);
-                } else {
-                    const uint32_t r01 = h01 & rest, r23 = h23 & rest;
-                    h01 = pack_bf16x2(p0 - bf16lo(r01), p1 - bf16hi(r01));
-                    h23 = pack_bf16x2(p2 - bf16lo(r23), p3 - bf16hi(r23));
-                }
-                const uint32_t b0 = transpose8(h01), b1 = transpose8(h23);
-                mma_bf16(o[g][0], c00, c01, c02, c03, b0, b1);
-                mma_bf16(o[g][1], c10, c11, c12, c13, b0, b1);
-                mma_bf16(off[g], k128, k128, k128, k128, b0, b1);
+                float acc[4] = {0.f, 0.f, 0.f, 0.f};
+                const uint32_t u0 = w0[g] >> 8, u1 = w1[g] >> 8;
+                mma_bf16(acc, code_pair(w0[g]), code_pair(w1[g]), code_pair16(w0[g]),
+                         code_pair16(w1[g]), bq[g][0], bq[g][1]);
+                mma_bf16(acc, code_pair(u0), code_pair(u1), code_pair16(u0), code_pair16(u1),
+                         bq[g][2], bq[g][3]);
+                const float s0 = bf16lo(m0[g]), s1 = bf16lo(m1[g]);
+                sc[0] = fmaf(s0, acc[0], sc[0]);
+                sc[1] = fmaf(s0, acc[1], sc[1]);
+                sc[2] = fmaf(s1, acc[2], sc[2]);
+                sc[3] = fmaf(s1, acc[3], sc[3]);
             }
         }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sc[e] *= A.scale_log2;
+        if (16 * t + 16 > nk) {                            // the sequence ends in this tile
+            if (16 * t + sr >= nk) sc[0] = sc[1] = -INFINITY;
+            if (16 * t + sr + 8 >= nk) sc[2] = sc[3] = -INFINITY;
+        }
+        uint32_t m0[NG], m1[NG];                           // V's (s, m)
+        load_words<NG>(m0, vsw + sr * NG);
+        load_words<NG>(m1, vsw + (sr + 8) * NG);
+        uint32_t smax = max_bf16x2(m0[0], m1[0]);
+#pragma unroll
+        for (int g = 1; g < NG; ++g) smax = max_bf16x2(smax, max_bf16x2(m0[g], m1[g]));
+
+        // ---- the references, where they have to move ----
+        const float top0 = fmaxf(sc[0], sc[2]), top1 = fmaxf(sc[1], sc[3]);
+        if (__any_sync(0xffffffffu, top0 > ref[0] + kSlack || top1 > ref[1] + kSlack ||
+                                        bf16lo(smax) >= cap)) {
+            float n0 = top0, n1 = top1;
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) {
+                n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, x));
+                n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, x));
+                smax = max_bf16x2(smax, __shfl_xor_sync(0xffffffffu, smax, x));
+            }
+            n0 = fmaxf(n0, ref[0]);
+            n1 = fmaxf(n1, ref[1]);
+            const uint32_t neb = max(eb, min(max((smax >> 7) & 0xffu, 17u), 244u));
+            // 2^(eb - neb), 0 at the first tile (where all sums are zero) and below 2^-126
+            const float es = neb - eb > 126u ? 0.f : __uint_as_float((127u - (neb - eb)) << 23);
+            const float f0 = ex2(ref[0] - n0), f1 = ex2(ref[1] - n1);
+            l[0] *= f0;
+            l[1] *= f1;
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                pm[g][0] *= f0;
+                pm[g][1] *= f1;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    o[g][e][0] *= f0 * es;
+                    o[g][e][1] *= f1 * es;
+                    o[g][e][2] *= f0 * es;
+                    o[g][e][3] *= f1 * es;
+                }
+            }
+            ref[0] = n0;
+            ref[1] = n1;
+            eb = neb;
+            up = __uint_as_float((259u - eb) << 23);                 // 2^(132 - eb)
+            cap = __uint_as_float((eb + 2u) << 23);                  // 4 times the step's power
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sc[e] = ex2(sc[e] - ref[e & 1]);
+        l[0] += sc[0] + sc[2];
+        l[1] += sc[1] + sc[3];
+
+        // ---- output: rows = coordinates, columns = heads ----
+        uint32_t wa[NG], wb[NG], wc[NG], wd[NG];
+        // rows 2 kk, 2 kk + 1, 2 kk + 8, 2 kk + 9 of the scores: keys kk + 0, 4, 8, 12
+        const uint32_t *vr = vw + kk * (S::RB / 4) + NG * (r >> 1);
+        load_words<NG>(wa, vr);
+        load_words<NG>(wb, vr + S::RB);
+        load_words<NG>(wc, vr + 2 * S::RB);
+        load_words<NG>(wd, vr + 3 * S::RB);
+        const float p0 = sc[0] * up, p1 = sc[1] * up, p2 = sc[2] * up, p3 = sc[3] * up;
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            const float s0 = bf16lo(m0[g]), s1 = bf16lo(m1[g]);
+            const float z0 = bf16hi(m0[g]), z1 = bf16hi(m1[g]);
+            pm[g][0] = fmaf(z0, sc[0], fmaf(z1, sc[2], pm[g][0]));
+            pm[g][1] = fmaf(z0, sc[1], fmaf(z1, sc[3], pm[g][1]));
+            const uint32_t b0 = transpose8(pack_f16x2(p0 * s0, p1 * s0));
+            const uint32_t b1 = transpose8(pack_f16x2(p2 * s1, p3 * s1));
+            const uint32_t y0 = __byte_perm(wa[g], wb[g], sel);
+            const uint32_t y1 = __byte_perm(wc[g], wd[g], sel);
+            const uint32_t u0 = y0 >> 8, u1 = y1 >> 8;
+            mma_f16(o[g][0], code_pair(y0), code_pair16(y0), code_pair(y1), code_pair16(y1), b0,
+                    b1);
+            mma_f16(o[g][1], code_pair(u0), code_pair16(u0), code_pair(u1), code_pair16(u1), b0,
+                    b1);
+        }
     }
-    __syncthreads();                   // every warp is done with the codes: partials go there
+
+    // ---- the warp's partials, over the rings ----
+    copy_wait<0>();
+    __syncthreads();
+    float *part = reinterpret_cast<float *>(smem);         // [warp][column][D + 4]
+    const float down = __uint_as_float((eb + 19u) << 23);            // 2^(eb - 108)
+    const float down16 = down * 0.0625f;
+#pragma unroll
+    for (int x = 4; x < 32; x <<= 1) {
+        l[0] += __shfl_xor_sync(0xffffffffu, l[0], x);
+        l[1] += __shfl_xor_sync(0xffffffffu, l[1], x);
+    }
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
         float d0 = pm[g][0], d1 = pm[g][1];
@@ -356,20 +452,26 @@ decode_q4_kernel(const DecQ4Args A) {
             d0 += __shfl_xor_sync(0xffffffffu, d0, x);
             d1 += __shfl_xor_sync(0xffffffffu, d1, x);
         }
-        d0 = (rest ? 0.f : d0) - off[g][0];
-        d1 = (rest ? 0.f : d1) - off[g][1];
         float *p0 = part + (warp * kCols + 2 * kk) * S::kPartStride + 16 * g + 2 * r;
         float *p1 = p0 + S::kPartStride;
-        *reinterpret_cast<float2 *>(p0) = make_float2(o[g][0][0] + d0, o[g][1][0] + d0);
-        *reinterpret_cast<float2 *>(p0 + D / 2) = make_float2(o[g][0][2] + d0, o[g][1][2] + d0);
-        *reinterpret_cast<float2 *>(p1) = make_float2(o[g][0][1] + d1, o[g][1][1] + d1);
-        *reinterpret_cast<float2 *>(p1 + D / 2) = make_float2(o[g][0][3] + d1, o[g][1][3] + d1);
+        if (2 * kk < G) {
+            *reinterpret_cast<float2 *>(p0) =
+                make_float2(fmaf(o[g][0][0], down, d0), fmaf(o[g][1][0], down, d0));
+            *reinterpret_cast<float2 *>(p0 + D / 2) =
+                make_float2(fmaf(o[g][0][2], down16, d0), fmaf(o[g][1][2], down16, d0));
+        }
+        if (2 * kk + 1 < G) {
+            *reinterpret_cast<float2 *>(p1) =
+                make_float2(fmaf(o[g][0][1], down, d1), fmaf(o[g][1][1], down, d1));
+            *reinterpret_cast<float2 *>(p1 + D / 2) =
+                make_float2(fmaf(o[g][0][3], down16, d1), fmaf(o[g][1][3], down16, d1));
+        }
     }
     if (r == 0) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            wml[(warp * kCols + 2 * kk + e) * 2] = mw[e];
-            wml[(warp * kCols + 2 * kk + e) * 2 + 1] = lw[e];
+            wml[(warp * kCols + 2 * kk + e) * 2] = ref[e];
+            wml[(warp * kCols + 2 * kk + e) * 2 + 1] = l[e];
         }
     }
     __syncthreads();
@@ -384,7 +486,7 @@ decode_q4_kernel(const DecQ4Args A) {
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
             const float m = wml[(w * kCols + tid) * 2];
-            const float f = m == -INFINITY ? 0.f : ex2(m - M);
+            const float f = ex2(m - M);                    // 0 for a warp without a tile
             sw[w * kCols + tid] = f;
             L = fmaf(f, wml[(w * kCols + tid) * 2 + 1], L);
         }
@@ -401,13 +503,8 @@ decode_q4_kernel(const DecQ4Args A) {
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
             const float f = sw[w * kCols + h];
-            float2 v = *reinterpret_cast<const float2 *>(part + (w * kCols + h) * S::kPartStride + d);
-            if constexpr (!WIDE) {
-                const float2 v2 = *reinterpret_cast<const float2 *>(
-                    part + (w * kCols + h + 4) * S::kPartStride + d);
-                v.x += v2.x;
-                v.y += v2.y;
-            }
+            const float2 v =
+                *reinterpret_cast<const float2 *>(part + (w * kCols + h) * S::kPartStride + d);
             a0 = fmaf(f, v.x, a0);
             a1 = fmaf(f, v.y, a1);
         }
@@ -512,10 +609,13 @@ decode_q4_merge_kernel(const float *__restrict__ ws_ml, const float *__restrict_
     }
 }
 
-// How a call is cut: heads per CTA, tiles per warp, chunks of a sequence.
+// How a call is cut: heads per CTA, slots per chunk, chunks of a sequence.
 struct Plan {
-    int G, n_sub, nt, n_splits;
+    int G, n_sub, chunk, n_splits;
 };
+
+constexpr int kSlots = 148 * 4;        // CTAs resident at once
+constexpr int kWaves = 3;              // and how many of each a full-length call should have
 
 Plan make_plan(int B, int Hq, int Hkv, int max_len) {
     Plan P;
@@ -523,19 +623,21 @@ Plan make_plan(int B, int Hq, int Hkv, int max_len) {
     P.n_sub = (g + kCols - 1) / kCols;
     P.G = (g + P.n_sub - 1) / P.n_sub;
     P.n_sub = (g + P.G - 1) / P.G;
-    const long long rows = (long long)B * Hkv * P.n_sub;
-    // Longer chunks leave fewer partials; shorter ones spread a small call over more
-    // SMs.  The longest that still gives every SM its four resident CTAs.
-    P.nt = 4;
-    while (P.nt > 1 && rows * ((max_len + 64 * P.nt - 1) / (64 * P.nt)) < 148 * 4) P.nt >>= 1;
-    P.n_splits = (max_len + 64 * P.nt - 1) / (64 * P.nt);
+    // Longer chunks leave less to merge, shorter ones spread a call evenly over the
+    // SMs: kWaves chunks for each place a CTA can have, of at least 64 slots (one tile
+    // for each warp).
+    const long long slots = (long long)B * Hkv * P.n_sub * max_len;
+    const long long even = (slots / (kSlots * kWaves) + 63) / 64 * 64;
+    const long long most = ((long long)max_len + 63) / 64 * 64;
+    P.chunk = (int)(even < 64 ? 64 : even > most ? most : even);
+    P.n_splits = (max_len + P.chunk - 1) / P.chunk;
     return P;
 }
 
-template <int D, int NT, bool WIDE>
-cudaError_t launch_split(const DecQ4Args &A, cudaStream_t s) {
-    using S = DecQ4Shape<D, NT>;
-    auto kern = decode_q4_kernel<D, NT, WIDE>;
+template <int D>
+cudaError_t launch_decode(const DecQ4Args &A, cudaStream_t s) {
+    using S = DecQ4Shape<D>;
+    auto kern = decode_q4_kernel<D>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          S::kSmem);
     if (e != cudaSuccess) return e;
@@ -549,27 +651,16 @@ cudaError_t launch_split(const DecQ4Args &A, cudaStream_t s) {
     cfg.stream = s;
     cfg.attrs = pdl;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, A);
-}
-
-template <int D>
-cudaError_t launch_decode(const DecQ4Args &A, int nt, cudaStream_t s) {
-    const bool wide = A.G > 4;
-    cudaError_t e;
-    switch (nt) {
-        case 1: e = wide ? launch_split<D, 1, true>(A, s) : launch_split<D, 1, false>(A, s); break;
-        case 2: e = wide ? launch_split<D, 2, true>(A, s) : launch_split<D, 2, false>(A, s); break;
-        default: e = wide ? launch_split<D, 4, true>(A, s) : launch_split<D, 4, false>(A, s); break;
-    }
+    e = cudaLaunchKernelEx(&cfg, kern, A);
     if (e != cudaSuccess || A.n_splits == 1) return e;
     const int rows = A.B * A.Hq;
     if (A.n_splits > 32)               // one group of 32 chunks is one warp's work
         return launch_pdl(decode_q4_merge_kernel<D, 4>, (unsigned)rows, 128, s,
                           (const float *)A.ws_ml, (const float *)A.ws_o, A.lens, A.max_len, A.Hq,
-                          A.Lmax, 64 * nt, A.n_splits, rows, A.out);
+                          A.Lmax, A.chunk, A.n_splits, rows, A.out);
     return launch_pdl(decode_q4_merge_kernel<D, 1>, (unsigned)((rows + 3) / 4), 128, s,
                       (const float *)A.ws_ml, (const float *)A.ws_o, A.lens, A.max_len, A.Hq,
-                      A.Lmax, 64 * nt, A.n_splits, rows, A.out);
+                      A.Lmax, A.chunk, A.n_splits, rows, A.out);
 }
 
 // ---------------------------------------------------------------------------
@@ -749,12 +840,13 @@ extern "C" gqa_status gqa_decode_q4(const void *q, const void *k_codes, const vo
     A.Hkv = Hkv;
     A.Lmax = Lmax;
     A.n_splits = P.n_splits;
+    A.chunk = P.chunk;
     A.n_sub = P.n_sub;
     A.G = P.G;
-    A.scale_log2 = (scale > 0.f ? scale : 1.0f / sqrtf((float)D)) * 1.4426950408889634f;
+    A.scale_log2 = (scale > 0.f ? scale : 1.0f / sqrtf((float)D)) * 1.4426950408889634f * 0x1p69f;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = D == 64   ? gqa::launch_decode<64>(A, P.nt, s)
-                          : D == 96 ? gqa::launch_decode<96>(A, P.nt, s)
-                                    : gqa::launch_decode<128>(A, P.nt, s);
+    const cudaError_t e = D == 64   ? gqa::launch_decode<64>(A, s)
+                          : D == 96 ? gqa::launch_decode<96>(A, s)
+                                    : gqa::launch_decode<128>(A, s);
     return e == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
 }

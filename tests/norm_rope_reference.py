@@ -133,14 +133,14 @@ def decode(q, cache, lens, scale=None):
 
     The tolerance counts the roundings of the scheme that the header of the kernel's
     source describes, each at its worst:
-      * a score is sum over groups of s (sum q (128 + c)) + (m - 128 s) sum q: products
-        exact, 32 + 2 additions each within U32 of the sum of magnitudes A_q =
-        sum |q| (143 s + |m| + 128 s), so off by d = 36 U32 A_q scale, and a few fp32
-        units of the score in the scaling and the exponential;
+      * a score is sum over groups of s sum(q c) + m sum(q): products exact (sum(q) in
+        24 bits), at most 36 additions each within U32 of the sum of magnitudes A_q =
+        sum |q| (15 s + |m|), so off by d = 36 U32 A_q scale, and a few fp32 units of
+        the score in the scaling and the exponential;
       * that moves p by up to 2 d of itself in numerator and denominator together;
-      * sum p s (128 + c) and 128 sum p s: p s in two bf16 parts, 2^-17 of each product
-        p s c, and additions over at most 64 keys of a warp and the merges within
-        80 U32 of sum p s 271; sum p m within 80 U32 of sum p |m|;
+      * p s is rounded once to fp16, 2^-12 of each product p s c with c <= 15; additions
+        over at most 64 keys of a warp and the merges within 80 U32 of
+        sum p (15 s + |m|);
       * the result's rounding to bf16, 2^-8 of it."""
     kc, ks, vc, vs = cache
     B, Hq, D = q.shape
@@ -158,11 +158,11 @@ def decode(q, cache, lens, scale=None):
             p = torch.softmax(sc, dim=-1)
             o = p @ V
             s_k, m_k = ks[b, h, :n].to(F64)[..., 0][:, grp], ks[b, h, :n].to(F64)[..., 1][:, grp]
-            mag = x.abs() @ (271 * s_k + m_k.abs()).T * scale
+            mag = x.abs() @ (15 * s_k + m_k.abs()).T * scale
             d = (36 * U32 * mag + 8 * U32 * (sc.abs() + 1)).amax(-1, keepdim=True)
             s_v, m_v = vs[b, h, :n].to(F64)[..., 0][:, grp], vs[b, h, :n].to(F64)[..., 1][:, grp]
-            e = 2 * d * (p @ V.abs()) + 2.0 ** -17 * 15 * (p @ s_v)
-            e = e + 80 * U32 * (p @ (271 * s_v + m_v.abs()))
+            e = 2 * d * (p @ V.abs()) + 2.0 ** -12 * 15 * (p @ s_v)
+            e = e + 80 * U32 * (p @ (15 * s_v + m_v.abs()))
             out[b, h * g:(h + 1) * g] = o
             tol[b, h * g:(h + 1) * g] = 2.0 ** -8 * o.abs() + 1.01 * e
     return out, tol

@@ -209,6 +209,16 @@ def test_host_tensors_are_refused():
 
 def test_gains_need_the_norm_and_axes_need_positions():
     with pytest.raises(ValueError, match="qk_norm"):
-        _lib._rope_inputs(1, 1, 64, torch.ones(64), None, None, None, False, None)
+        _lib._rope_spec(1, 1, 64, torch.ones(64), None, None, None, False)
     with pytest.raises(ValueError, match="pos"):
-        _lib._rope_inputs(1, 1, 64, None, None, None, gqa.RopeAxes((32,)), True, None)
+        _lib._rope_spec(1, 1, 64, None, None, None, gqa.RopeAxes((32,)), True)
+
+
+def test_native_argument_checks_leave_host_tensors_to_the_slow_path(lib):
+    from rope_gqa_kv_b200 import _fastargs
+    t = torch.zeros(2, 3)
+    assert _fastargs.pointers(0, ("t", t, torch.float32, (2, 3))) is None
+    assert _fastargs.pointers(0, ("t", "text", torch.float32, (2, 3))) is None
+    for bad in ((0,), (0, ("t", t)), ("x", ()), (0, ["t", t, None, None])):
+        with pytest.raises(TypeError):
+            _fastargs.pointers(*bad)
