@@ -30,7 +30,8 @@
  *     Lmax is a multiple of 128.  Every data pointer is 16-byte aligned.
  *   - All pointers except the stream are DEVICE pointers to caller-owned memory.
  *     The library allocates no memory and keeps no per-call state; it caches
- *     one function pointer (the driver's tensor-map encoder) per process.
+ *     one function pointer (the driver's tensor-map encoder) per process and, per
+ *     host thread, the rotation frequencies of the last gqa_rope_params.
  *   - stream is a cudaStream_t (NULL = legacy default stream).  All work is
  *     queued asynchronously on it; the host return code covers argument
  *     validation and launch errors only.
@@ -431,9 +432,10 @@ gqa_status kv_cache_read_q4(const void *k_codes, const void *k_scales, const voi
 /*
  * gqa_decode_q4 -- gqa_decode against a 4-bit cache; K and V are the values
  * m + s c, not rounded to bf16.  Lengths, errors and the workspace's rules as
- * there; gqa_decode_q4_workspace_bytes gives its size (a cut of the sequences that
- * needs no merge wants none; 16 bytes are named then).  Values of magnitude up to
- * 2^110 are handled (sums of larger ones can overflow).
+ * there; gqa_decode_q4_workspace_bytes gives its size (where one chunk covers
+ * max_len_host nothing is merged and no workspace is used; 16 bytes are named then).
+ * The chunks' length follows from B, the heads and max_len_host.  Queries and values
+ * of magnitude up to 2^60 and 2^110 are handled (sums of larger ones can overflow).
  */
 gqa_status gqa_decode_q4(const void *q, const void *k_codes, const void *k_scales,
                          const void *v_codes, const void *v_scales, const int32_t *lens,

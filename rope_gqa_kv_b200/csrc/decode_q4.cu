@@ -30,13 +30,16 @@
 // times the bytes that arrived, for 8 columns of work.
 //
 // Work: one CTA per (chunk of the cached slots, KV head x head subgroup, sequence).
-// Its four warps take the chunk's 16-key tiles in turn, each through a ring of its own
-// (asynchronous 16-byte copies, kStages tiles deep; no warp waits for another), with a
+// Its four warps take the chunk's units of U 16-key tiles in turn, each through a ring
+// of its own (asynchronous 16-byte copies; no warp waits for another), with a
 // running softmax: the reference moves, and what is summed is scaled down, only when a
 // score passes it by more than 8, i.e. hardly ever after the first tile.  At the end
 // the warps' statistics and partial outputs are merged in shared memory, the chunk's
 // (m, l, o) goes to the workspace and a second kernel, a programmatic dependent,
 // merges the chunks.  When one chunk covers max_len the CTA writes the output itself.
+#include <atomic>
+#include <type_traits>
+
 #include "q4.cuh"
 #include "ptx.cuh"
 #include "rope.cuh"
@@ -47,7 +50,6 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kCols = 8;               // columns of the mma: query heads of a CTA, at most
-constexpr int kStages = 4;             // tiles of a warp's ring
 constexpr float kSlack = 8.0f;         // a score may pass the softmax reference by this
 constexpr float kNoRef = -1e30f;       // the reference before any score: finite, so that
                                        // 2^(a score of -inf - it) is 0
@@ -59,6 +61,14 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
         "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// The same with 8 columns of the first operand.
+__device__ __forceinline__ void mma_bf16_k8(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k8.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
+        "{%4, %5}, {%6}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(b0));
 }
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                         uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -122,17 +132,23 @@ __device__ __forceinline__ void copy_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-template <int D>
+// U: tiles (of 16 keys) that a warp takes at a time.
+template <int D, int U>
 struct DecQ4Shape {
     static constexpr int NG = Q4Shape<D>::NG;
     static constexpr int RB = D / 2;                       // bytes of codes per row
     static constexpr int SB = 4 * NG;                      // bytes of scales per row
-    // A tile in the ring: [K codes][V codes][K scales][V scales], 16 rows each.
-    static constexpr int kOffV = 16 * RB;
-    static constexpr int kOffKS = 32 * RB;
-    static constexpr int kOffVS = 32 * RB + 16 * SB;
-    static constexpr int kTile = 32 * (RB + SB);
-    static constexpr int kRing = kWarps * kStages * kTile;
+    static constexpr int R = 16 * U;                       // rows of a unit
+    static constexpr int kStages = U == 1 ? 4 : 3;         // units of a warp's ring
+    // Bytes from row to row in the ring.  D = 128: 80, so that neither the two rows
+    // that eight lanes read of K nor the four they read of V meet in a bank.
+    static constexpr int RS = D == 128 ? 80 : RB;
+    // A unit in the ring: [K codes][V codes][K scales][V scales].
+    static constexpr int kOffV = R * RS;
+    static constexpr int kOffKS = 2 * R * RS;
+    static constexpr int kOffVS = 2 * R * RS + R * SB;
+    static constexpr int kUnit = 2 * R * (RS + SB);
+    static constexpr int kRing = kWarps * kStages * kUnit;
     // The warps' partial outputs (kWarps x kCols x (D + 4) f32) are written over the
     // rings once every warp is done.  D + 4: the four lanes of a row write four
     // columns, 8 banks apart.
@@ -156,11 +172,11 @@ struct DecQ4Args {
 
 // Workspace: [(m, l): rows x 2 f32][o: rows x D f32], rows = B x Hq x n_splits, row
 // (b, h, c) = (b * Hq + h) * n_splits + c.
-template <int D>
-__global__ void __launch_bounds__(kThreads, 4)
+template <int D, int U>
+__global__ void __launch_bounds__(kThreads, U == 1 ? 4 : 3)
 decode_q4_kernel(const DecQ4Args A) {
-    using S = DecQ4Shape<D>;
-    constexpr int NG = S::NG;
+    using S = DecQ4Shape<D, U>;
+    constexpr int NG = S::NG, kStages = S::kStages;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float wml[kWarps * kCols * 2];              // (m, l) [warp][column]
     __shared__ float sw[kWarps * kCols];                   // merge weights [warp][column]
@@ -190,58 +206,65 @@ decode_q4_kernel(const DecQ4Args A) {
     const int nk = min(A.chunk, len - key0);
 
     // ---- the warp's ring ----
-    // A lane copies 16 bytes of each 512-byte block of codes, and 16 of the scales:
-    // lanes 0 .. 15 K's, lanes 16 .. 31 V's.
-    const size_t row = ((size_t)b * A.Hkv + kvh) * A.Lmax + key0;
+    // A lane copies 16 bytes of each 512-byte block of codes, and 16 of each 256 of the
+    // scales: lanes 0 .. 15 K's, lanes 16 .. 31 V's.
+    const size_t row = ((size_t)b * A.Hkv + kvh) * A.Lmax + key0 + warp * S::R;
     const uint8_t *kg = A.kc + row * S::RB + 16 * lane, *vg = A.vc + row * S::RB + 16 * lane;
     const uint8_t *sg = reinterpret_cast<const uint8_t *>(lane < 16 ? A.ks : A.vs) +
                         row * S::SB + 16 * (lane & 15);
-    const uint32_t ring = ptx::smem_addr(smem) + warp * (kStages * S::kTile) + 16 * lane;
-    const uint32_t ring_s = ring + S::kOffKS + (lane < 16 ? 0 : 16 * S::SB - 256);
-    const int n_tiles = (nk + 15) >> 4;
-    // Tile t (keys 16 t ..) to a stage.  The rows behind the length are not read: their
+    const uint32_t ring = ptx::smem_addr(smem) + warp * (kStages * S::kUnit);
+    const int n_units = (nk + S::R - 1) / S::R;
+    // Unit u, the warp's next, to a stage.  The rows behind the length are not read: their
     // codes and scales are zeros.
-    auto fetch = [&](int t, int stage) {
-        const uint8_t *k = kg + (size_t)t * (16 * S::RB), *v = vg + (size_t)t * (16 * S::RB);
-        const uint8_t *s = sg + (size_t)t * (16 * S::SB);
-        const uint32_t dst = ring + stage * S::kTile, dst_s = ring_s + stage * S::kTile;
-        if (16 * t + 16 <= nk) {                           // uniform across the warp
+    auto copy = [&](uint32_t dst, int live, auto full) {   // full: no row is behind the length
 #pragma unroll
-            for (int x = 0; x < 16 * S::RB; x += 512)
-                if (x + 512 <= 16 * S::RB || x + 16 * lane < 16 * S::RB) {
-                    copy16(dst + x, k + x);
-                    copy16(dst + S::kOffV + x, v + x);
-                }
-            if ((lane & 15) < S::SB) copy16(dst_s, s);
-        } else {
-            const int live = nk - 16 * t;
-#pragma unroll
-            for (int x = 0; x < 16 * S::RB; x += 512)
-                if (x + 512 <= 16 * S::RB || x + 16 * lane < 16 * S::RB) {
-                    const int n = min(16, max(0, live * S::RB - x - 16 * lane));
-                    copy16(dst + x, k + x, n);
-                    copy16(dst + S::kOffV + x, v + x, n);
-                }
-            if ((lane & 15) < S::SB)
-                copy16(dst_s, s, min(16, max(0, live * S::SB - 16 * (lane & 15))));
+        for (int x = 0; x < S::R * S::RB; x += 512) {
+            const int at = x + 16 * lane;                  // in the unit's codes
+            if (x + 512 <= S::R * S::RB || at < S::R * S::RB) {
+                const uint32_t to = dst + at / S::RB * S::RS + at % S::RB;
+                const int n = full ? 16 : min(16, max(0, live * S::RB - at));
+                copy16(to, kg + x, n);
+                copy16(to + S::kOffV, vg + x, n);
+            }
         }
+#pragma unroll
+        for (int x = 0; x < S::R * S::SB; x += 256) {
+            const int at = x + 16 * (lane & 15);
+            if (x + 256 <= S::R * S::SB || at < S::R * S::SB)
+                copy16(dst + (lane < 16 ? S::kOffKS : S::kOffVS) + at, sg + x,
+                       full ? 16 : min(16, max(0, live * S::SB - at)));
+        }
+    };
+    auto fetch = [&](int u, int stage) {
+        const int live = nk - S::R * u;                    // uniform across the warp
+        if (live >= S::R)
+            copy(ring + stage * S::kUnit, live, std::true_type{});
+        else
+            copy(ring + stage * S::kUnit, live, std::false_type{});
+        kg += S::R * kWarps * S::RB;
+        vg += S::R * kWarps * S::RB;
+        sg += S::R * kWarps * S::SB;
     };
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) {
-        if (warp + kWarps * i < n_tiles) fetch(warp + kWarps * i, i);
+        if (warp + kWarps * i < n_units) fetch(warp + kWarps * i, i);
         copy_commit();
     }
 
     const int r = lane >> 2, kk = lane & 3;
     // Row r of a product's first eight is key sr of the tile, row r + 8 key sr + 8: any
-    // order serves, and with this one the four rows that a load of V touches are
-    // neighbours, which fall into different banks.
-    const int sr = (r >> 1) + 4 * (r & 1);
+    // order serves.  With these, what the lanes of one access read lies in different
+    // banks: rows (i, i + 4) of K together, or (D = 64) any four neighbours in r, and
+    // the rows va (and vb) of V for kk = 0 .. 3.
+    const int sr = D == 64 ? ((r >> 1) & 1) + 2 * ((r & 1) ^ (r >> 2)) + (r & 4)
+                           : (r >> 1) + 4 * (r & 1);
+    const int va = D == 64 ? (kk & 1) + 6 * (kk >> 1) : kk;          // sr of r = 2 kk
+    const int vb = D == 64 ? kk + 2 : kk + 4;                        // sr of r = 2 kk + 1
     // q as the 8-column operand: column r is head r.  Word kk of group g covers
     // coordinates 16 g + 4 kk .. + 3 and their partners in the second half; its codes
     // come as coordinates (0, 2) of the first half, of the second (times 16), and,
     // shifted down by 8, (1, 3) of the first, of the second (times 16).
-    uint32_t bq[NG][4];
+    uint4 bqr[NG];
     uint32_t bm[3];                    // sum of q over group kk, head r: bf16 parts, high half
     {
         const uint16_t *q = A.q + ((size_t)b * A.Hq + h0 + r) * D + 4 * kk;
@@ -259,21 +282,19 @@ decode_q4_kernel(const DecQ4Args A) {
         for (int i = 0; i < 8; ++i) qsum[i] = 0.f;
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
-            bq[g][0] = __byte_perm(lo[g].x, lo[g].y, 0x5410);
-            bq[g][1] = __byte_perm(hi[g].x, hi[g].y, 0x5410);
-            bq[g][2] = __byte_perm(lo[g].x, lo[g].y, 0x7632);
-            bq[g][3] = __byte_perm(hi[g].x, hi[g].y, 0x7632);
+            const uint32_t b0 = __byte_perm(lo[g].x, lo[g].y, 0x5410);
+            const uint32_t b1 = __byte_perm(hi[g].x, hi[g].y, 0x5410);
+            const uint32_t b2 = __byte_perm(lo[g].x, lo[g].y, 0x7632);
+            const uint32_t b3 = __byte_perm(hi[g].x, hi[g].y, 0x7632);
             float acc[4] = {0.f, 0.f, 0.f, 0.f};
             constexpr uint32_t one = 0x3f803f80u;
-            mma_bf16(acc, one, one, one, one, bq[g][0], bq[g][1]);
-            mma_bf16(acc, one, one, one, one, bq[g][2], bq[g][3]);
+            mma_bf16(acc, one, one, one, one, b0, b1);
+            mma_bf16(acc, one, one, one, one, b2, b3);
             qsum[2 * g] = acc[0];
             qsum[2 * g + 1] = acc[1];
             constexpr uint32_t up64 = 0x5f805f80u, up60 = 0x5d805d80u;   // 2^64, 2^60 twice
-            bq[g][0] = mul_bf16x2(bq[g][0], up64);
-            bq[g][1] = mul_bf16x2(bq[g][1], up60);
-            bq[g][2] = mul_bf16x2(bq[g][2], up64);
-            bq[g][3] = mul_bf16x2(bq[g][3], up60);
+            bqr[g] = make_uint4(mul_bf16x2(b0, up64), mul_bf16x2(b1, up60),
+                                         mul_bf16x2(b2, up64), mul_bf16x2(b3, up60));
         }
         // Every row r of the sums is alike: lane (r, k) offers group r / 2 of head
         // 2 k + r % 2, and fetches group kk of head r.
@@ -309,76 +330,90 @@ decode_q4_kernel(const DecQ4Args A) {
 
     int stage = 0;
 #pragma unroll 1
-    for (int t = warp; t < n_tiles; t += kWarps) {
+    for (int u = warp; u < n_units; u += kWarps) {
         copy_wait<kStages - 2>();
         __syncwarp();
         {
-            const int ahead = t + kWarps * (kStages - 1);  // into the stage read last
-            if (ahead < n_tiles) fetch(ahead, (stage + kStages - 1) % kStages);
+            const int ahead = u + kWarps * (kStages - 1);  // into the stage read last
+            if (ahead < n_units) fetch(ahead, stage == 0 ? kStages - 1 : stage - 1);
             copy_commit();
         }
-        const uint8_t *tile = smem + (warp * kStages + stage) * S::kTile;
-        stage = (stage + 1) % kStages;
-        const uint32_t *kw = reinterpret_cast<const uint32_t *>(tile);
-        const uint32_t *vw = reinterpret_cast<const uint32_t *>(tile + S::kOffV);
-        const uint32_t *ksw = reinterpret_cast<const uint32_t *>(tile + S::kOffKS);
-        const uint32_t *vsw = reinterpret_cast<const uint32_t *>(tile + S::kOffVS);
+        const uint8_t *unit = smem + (warp * kStages + stage) * S::kUnit;
+        stage = stage == kStages - 1 ? 0 : stage + 1;
+        const uint32_t *kw = reinterpret_cast<const uint32_t *>(unit);
+        const uint32_t *vw = reinterpret_cast<const uint32_t *>(unit + S::kOffV);
+        const uint32_t *ksw = reinterpret_cast<const uint32_t *>(unit + S::kOffKS);
+        const uint32_t *vsw = reinterpret_cast<const uint32_t *>(unit + S::kOffVS);
 
-        // ---- scores: lane (r, kk) has rows r and r + 8 against its two columns ----
-        float sc[4] = {0.f, 0.f, 0.f, 0.f};
-        {
-            uint32_t w0[NG], w1[NG], m0[NG], m1[NG];
-            load_words<NG>(w0, kw + sr * (S::RB / 4) + NG * kk);
-            load_words<NG>(w1, kw + (sr + 8) * (S::RB / 4) + NG * kk);
-            load_words<NG>(m0, ksw + sr * NG);
-            load_words<NG>(m1, ksw + (sr + 8) * NG);
-            const uint32_t mk0 = ksw[sr * NG + min(kk, NG - 1)];
-            const uint32_t mk1 = ksw[(sr + 8) * NG + min(kk, NG - 1)];
-            mma_bf16(sc, mk0, mk1, mk0, mk1, bm[0], bm[1]);
-            mma_bf16(sc, mk0, mk1, mk0, mk1, bm[2], 0u);
+        // ---- scores: lane (r, kk) has rows r and r + 8 of a tile against its columns ----
+        float sc[U][4];
+        uint32_t m0[U][NG], m1[U][NG];                     // V's (s, m)
+        uint32_t smax = 0;
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            const int k0 = 16 * j + sr, k1 = k0 + 8;
+            uint32_t w0[NG], w1[NG], x0[NG], x1[NG];
+            load_words<NG>(w0, kw + k0 * (S::RS / 4) + NG * kk);
+            load_words<NG>(w1, kw + k1 * (S::RS / 4) + NG * kk);
+            load_words<NG>(x0, ksw + k0 * NG);
+            load_words<NG>(x1, ksw + k1 * NG);
+            const uint32_t mk0 = ksw[k0 * NG + min(kk, NG - 1)];
+            const uint32_t mk1 = ksw[k1 * NG + min(kk, NG - 1)];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sc[j][e] = 0.f;
+#pragma unroll
+            for (int x = 0; x < 3; ++x) mma_bf16_k8(sc[j], mk0, mk1, bm[x]);
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
                 float acc[4] = {0.f, 0.f, 0.f, 0.f};
                 const uint32_t u0 = w0[g] >> 8, u1 = w1[g] >> 8;
                 mma_bf16(acc, code_pair(w0[g]), code_pair(w1[g]), code_pair16(w0[g]),
-                         code_pair16(w1[g]), bq[g][0], bq[g][1]);
+                         code_pair16(w1[g]), bqr[g].x, bqr[g].y);
                 mma_bf16(acc, code_pair(u0), code_pair(u1), code_pair16(u0), code_pair16(u1),
-                         bq[g][2], bq[g][3]);
-                const float s0 = bf16lo(m0[g]), s1 = bf16lo(m1[g]);
-                sc[0] = fmaf(s0, acc[0], sc[0]);
-                sc[1] = fmaf(s0, acc[1], sc[1]);
-                sc[2] = fmaf(s1, acc[2], sc[2]);
-                sc[3] = fmaf(s1, acc[3], sc[3]);
+                         bqr[g].z, bqr[g].w);
+                const float s0 = bf16lo(x0[g]), s1 = bf16lo(x1[g]);
+                sc[j][0] = fmaf(s0, acc[0], sc[j][0]);
+                sc[j][1] = fmaf(s0, acc[1], sc[j][1]);
+                sc[j][2] = fmaf(s1, acc[2], sc[j][2]);
+                sc[j][3] = fmaf(s1, acc[3], sc[j][3]);
+            }
+            load_words<NG>(m0[j], vsw + k0 * NG);
+            load_words<NG>(m1[j], vsw + k1 * NG);
+            smax = max_bf16x2(smax, max_bf16x2(vsw[k0 * NG + min(kk, NG - 1)],
+                                               vsw[k1 * NG + min(kk, NG - 1)]));
+        }
+        if (S::R * (u + 1) > nk) {                         // the sequence ends in this unit
+#pragma unroll
+            for (int j = 0; j < U; ++j) {
+                if (S::R * u + 16 * j + sr >= nk) sc[j][0] = sc[j][1] = -INFINITY;
+                if (S::R * u + 16 * j + sr + 8 >= nk) sc[j][2] = sc[j][3] = -INFINITY;
             }
         }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sc[e] *= A.scale_log2;
-        if (16 * t + 16 > nk) {                            // the sequence ends in this tile
-            if (16 * t + sr >= nk) sc[0] = sc[1] = -INFINITY;
-            if (16 * t + sr + 8 >= nk) sc[2] = sc[3] = -INFINITY;
-        }
-        uint32_t m0[NG], m1[NG];                           // V's (s, m)
-        load_words<NG>(m0, vsw + sr * NG);
-        load_words<NG>(m1, vsw + (sr + 8) * NG);
-        uint32_t smax = max_bf16x2(m0[0], m1[0]);
-#pragma unroll
-        for (int g = 1; g < NG; ++g) smax = max_bf16x2(smax, max_bf16x2(m0[g], m1[g]));
 
         // ---- the references, where they have to move ----
-        const float top0 = fmaxf(sc[0], sc[2]), top1 = fmaxf(sc[1], sc[3]);
-        if (__any_sync(0xffffffffu, top0 > ref[0] + kSlack || top1 > ref[1] + kSlack ||
+        float n0 = fmaxf(sc[0][0], sc[0][2]), n1 = fmaxf(sc[0][1], sc[0][3]);
+#pragma unroll
+        for (int j = 1; j < U; ++j) {
+            n0 = fmaxf(n0, fmaxf(sc[j][0], sc[j][2]));
+            n1 = fmaxf(n1, fmaxf(sc[j][1], sc[j][3]));
+        }
+        n0 *= A.scale_log2;
+        n1 *= A.scale_log2;
+        // (the lanes of a row hold one group's step each)
+        if (__any_sync(0xffffffffu, fmaxf(n0 - ref[0], n1 - ref[1]) > kSlack ||
                                         bf16lo(smax) >= cap)) {
-            float n0 = top0, n1 = top1;
 #pragma unroll
             for (int x = 4; x < 32; x <<= 1) {
                 n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, x));
                 n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, x));
-                smax = max_bf16x2(smax, __shfl_xor_sync(0xffffffffu, smax, x));
             }
+#pragma unroll
+            for (int x = 1; x < 32; x <<= 1)
+                smax = max_bf16x2(smax, __shfl_xor_sync(0xffffffffu, smax, x));
             n0 = fmaxf(n0, ref[0]);
             n1 = fmaxf(n1, ref[1]);
-            const uint32_t neb = max(eb, min(max((smax >> 7) & 0xffu, 17u), 244u));
-            // 2^(eb - neb), 0 at the first tile (where all sums are zero) and below 2^-126
+            const uint32_t neb = max(eb, min(max((smax >> 7) & 0xffu, 17u), 235u));
+            // 2^(eb - neb), 0 at the first unit (where all sums are zero) and below 2^-126
             const float es = neb - eb > 126u ? 0.f : __uint_as_float((127u - (neb - eb)) << 23);
             const float f0 = ex2(ref[0] - n0), f1 = ex2(ref[1] - n1);
             l[0] *= f0;
@@ -401,35 +436,39 @@ decode_q4_kernel(const DecQ4Args A) {
             up = __uint_as_float((259u - eb) << 23);                 // 2^(132 - eb)
             cap = __uint_as_float((eb + 2u) << 23);                  // 4 times the step's power
         }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sc[e] = ex2(sc[e] - ref[e & 1]);
-        l[0] += sc[0] + sc[2];
-        l[1] += sc[1] + sc[3];
 
         // ---- output: rows = coordinates, columns = heads ----
-        uint32_t wa[NG], wb[NG], wc[NG], wd[NG];
-        // rows 2 kk, 2 kk + 1, 2 kk + 8, 2 kk + 9 of the scores: keys kk + 0, 4, 8, 12
-        const uint32_t *vr = vw + kk * (S::RB / 4) + NG * (r >> 1);
-        load_words<NG>(wa, vr);
-        load_words<NG>(wb, vr + S::RB);
-        load_words<NG>(wc, vr + 2 * S::RB);
-        load_words<NG>(wd, vr + 3 * S::RB);
-        const float p0 = sc[0] * up, p1 = sc[1] * up, p2 = sc[2] * up, p3 = sc[3] * up;
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
-            const float s0 = bf16lo(m0[g]), s1 = bf16lo(m1[g]);
-            const float z0 = bf16hi(m0[g]), z1 = bf16hi(m1[g]);
-            pm[g][0] = fmaf(z0, sc[0], fmaf(z1, sc[2], pm[g][0]));
-            pm[g][1] = fmaf(z0, sc[1], fmaf(z1, sc[3], pm[g][1]));
-            const uint32_t b0 = transpose8(pack_f16x2(p0 * s0, p1 * s0));
-            const uint32_t b1 = transpose8(pack_f16x2(p2 * s1, p3 * s1));
-            const uint32_t y0 = __byte_perm(wa[g], wb[g], sel);
-            const uint32_t y1 = __byte_perm(wc[g], wd[g], sel);
-            const uint32_t u0 = y0 >> 8, u1 = y1 >> 8;
-            mma_f16(o[g][0], code_pair(y0), code_pair16(y0), code_pair(y1), code_pair16(y1), b0,
-                    b1);
-            mma_f16(o[g][1], code_pair(u0), code_pair16(u0), code_pair(u1), code_pair16(u1), b0,
-                    b1);
+        for (int j = 0; j < U; ++j) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sc[j][e] = ex2(fmaf(sc[j][e], A.scale_log2, -ref[e & 1]));
+            l[0] += sc[j][0] + sc[j][2];
+            l[1] += sc[j][1] + sc[j][3];
+            uint32_t wa[NG], wb[NG], wc[NG], wd[NG];       // rows 2 kk, 2 kk + 1, and 8 on
+            const uint32_t *vr = vw + 16 * j * (S::RS / 4) + NG * (r >> 1);
+            load_words<NG>(wa, vr + va * (S::RS / 4));
+            load_words<NG>(wb, vr + vb * (S::RS / 4));
+            load_words<NG>(wc, vr + (va + 8) * (S::RS / 4));
+            load_words<NG>(wd, vr + (vb + 8) * (S::RS / 4));
+            const float p0 = sc[j][0] * up, p1 = sc[j][1] * up;
+            const float p2 = sc[j][2] * up, p3 = sc[j][3] * up;
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                const float s0 = bf16lo(m0[j][g]), s1 = bf16lo(m1[j][g]);
+                const float z0 = bf16hi(m0[j][g]), z1 = bf16hi(m1[j][g]);
+                pm[g][0] = fmaf(z0, sc[j][0], fmaf(z1, sc[j][2], pm[g][0]));
+                pm[g][1] = fmaf(z0, sc[j][1], fmaf(z1, sc[j][3], pm[g][1]));
+                const uint32_t b0 = transpose8(pack_f16x2(p0 * s0, p1 * s0));
+                const uint32_t b1 = transpose8(pack_f16x2(p2 * s1, p3 * s1));
+                // Rows r + 8 get the whole bytes, 16 times the upper code plus the lower:
+                // one instruction fewer, and the lower ones' sums are in rows r.
+                const uint32_t y0 = __byte_perm(wa[g], wb[g], sel);
+                const uint32_t y1 = __byte_perm(wc[g], wd[g], sel);
+                const uint32_t u0 = __byte_perm(y0, 0u, 0x4341), u1 = __byte_perm(y1, 0u, 0x4341);
+                mma_f16(o[g][0], code_pair(y0), y0 & 0x00ff00ffu, code_pair(y1), y1 & 0x00ff00ffu,
+                        b0, b1);
+                mma_f16(o[g][1], code_pair(u0), u0, code_pair(u1), u1, b0, b1);
+            }
         }
     }
 
@@ -458,13 +497,15 @@ decode_q4_kernel(const DecQ4Args A) {
             *reinterpret_cast<float2 *>(p0) =
                 make_float2(fmaf(o[g][0][0], down, d0), fmaf(o[g][1][0], down, d0));
             *reinterpret_cast<float2 *>(p0 + D / 2) =
-                make_float2(fmaf(o[g][0][2], down16, d0), fmaf(o[g][1][2], down16, d0));
+                make_float2(fmaf(o[g][0][2] - o[g][0][0], down16, d0),
+                            fmaf(o[g][1][2] - o[g][1][0], down16, d0));
         }
         if (2 * kk + 1 < G) {
             *reinterpret_cast<float2 *>(p1) =
                 make_float2(fmaf(o[g][0][1], down, d1), fmaf(o[g][1][1], down, d1));
             *reinterpret_cast<float2 *>(p1 + D / 2) =
-                make_float2(fmaf(o[g][0][3], down16, d1), fmaf(o[g][1][3], down16, d1));
+                make_float2(fmaf(o[g][0][3] - o[g][0][1], down16, d1),
+                            fmaf(o[g][1][3] - o[g][1][1], down16, d1));
         }
     }
     if (r == 0) {
@@ -615,6 +656,7 @@ struct Plan {
 };
 
 constexpr int kSlots = 148 * 4;        // CTAs resident at once
+constexpr int kLongChunk = 256;        // slots from which a warp takes two tiles at a time
 constexpr int kWaves = 3;              // and how many of each a full-length call should have
 
 Plan make_plan(int B, int Hq, int Hkv, int max_len) {
@@ -634,13 +676,10 @@ Plan make_plan(int B, int Hq, int Hkv, int max_len) {
     return P;
 }
 
-template <int D>
-cudaError_t launch_decode(const DecQ4Args &A, cudaStream_t s) {
-    using S = DecQ4Shape<D>;
-    auto kern = decode_q4_kernel<D>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         S::kSmem);
-    if (e != cudaSuccess) return e;
+template <int D, int U>
+cudaError_t launch_split(const DecQ4Args &A, cudaStream_t s) {
+    using S = DecQ4Shape<D, U>;
+    auto kern = decode_q4_kernel<D, U>;
     cudaLaunchAttribute pdl[1];
     pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     pdl[0].val.programmaticStreamSerializationAllowed = 1;
@@ -651,7 +690,29 @@ cudaError_t launch_decode(const DecQ4Args &A, cudaStream_t s) {
     cfg.stream = s;
     cfg.attrs = pdl;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, kern, A);
+    // The kernel's limit of shared memory is raised once per device; a context that does
+    // not know of it yet refuses the launch.
+    static std::atomic<uint64_t> raised{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (raised.load(std::memory_order_relaxed) & bit) {
+        e = cudaLaunchKernelEx(&cfg, kern, A);
+        if (e != cudaErrorInvalidValue) return e;
+        cudaGetLastError();
+    }
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    if (e != cudaSuccess) return e;
+    raised.fetch_or(bit, std::memory_order_relaxed);
+    return cudaLaunchKernelEx(&cfg, kern, A);
+}
+
+template <int D>
+cudaError_t launch_decode(const DecQ4Args &A, cudaStream_t s) {
+    // Two tiles at a time where each warp has several: fewer instructions a tile.
+    const cudaError_t e = A.chunk >= kLongChunk ? launch_split<D, 2>(A, s)
+                                                : launch_split<D, 1>(A, s);
     if (e != cudaSuccess || A.n_splits == 1) return e;
     const int rows = A.B * A.Hq;
     if (A.n_splits > 32)               // one group of 32 chunks is one warp's work

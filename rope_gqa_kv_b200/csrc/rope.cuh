@@ -138,7 +138,7 @@ __device__ __forceinline__ void rotate_vector(const uint4 a_in, const uint4 b_in
 }
 
 // theta_i for the chosen variant, in float64 on the host (formulas in gqa.h).
-inline RopeTable make_table(int D, const gqa_rope_params &p) {
+inline RopeTable compute_table(int D, const gqa_rope_params &p) {
     RopeTable t;
     const int half = D / 2;
     const double base = (double)p.rope_base, s = (double)p.factor;
@@ -161,6 +161,26 @@ inline RopeTable make_table(int D, const gqa_rope_params &p) {
     }
     t.mscale = p.scaling == GQA_ROPE_YARN ? (float)(0.1 * std::log(s) + 1.0) : 1.0f;
     return t;
+}
+
+// The same, computed again only when D or the parameters change: the 32 to 64 powers
+// take about as long as a launch.
+inline const RopeTable &make_table(int D, const gqa_rope_params &p) {
+    struct Last {
+        int D = 0;
+        gqa_rope_params p = {};
+        RopeTable t = {};
+    };
+    static thread_local Last last;
+    const gqa_rope_params &q = last.p;
+    if (last.D != D || q.rope_base != p.rope_base || q.scaling != p.scaling ||
+        q.factor != p.factor || q.original_max_pos != p.original_max_pos ||
+        q.yarn_alpha != p.yarn_alpha || q.yarn_beta != p.yarn_beta) {
+        last.t = compute_table(D, p);
+        last.D = D;
+        last.p = p;
+    }
+    return last.t;
 }
 
 // A launch as a programmatic dependent of the preceding kernel on the stream: its
