@@ -7,14 +7,16 @@
 //   on pair i's axis (image and video tokens: time, height, width).
 //
 // Forward.  Bound by memory: q is read and written once, k and v read once, the
-// cache rows written once.  A warp takes one token (or, when there are few tokens,
-// one slice of a token's vectors, so that a decode step still spreads over the
-// SMs); it walks the token's Hq query, Hkv key and Hkv value vectors kVecPerWarp at
-// a time, kAhead passes loaded before any is used, the first ones before the angles
-// are computed.  A vector is held by 4 or 8 lanes, lane j with coordinates
+// cache rows written once.  A vector is held by 4 or 8 lanes, lane j with coordinates
 // 8j .. 8j+7 and D/2 + 8j ..: both members of its 8 rotation pairs, and half of one
 // group of the 4-bit row, so rotation needs no exchange, the norm one shuffle sum
-// and the quantiser one shuffle per group.
+// and the quantiser one shuffle per group.  A warp takes one token at a time (or, when
+// there are few tokens, one slice of a token's vectors, so that a decode step still
+// spreads over the SMs); it walks the token's query, key and value vectors
+// kVecPerWarp at a time, a pass of one kind each.  What a lane needs of the next kRing
+// passes, those of the warp's next tokens included, is on its way into the lane's own
+// places of a shared-memory ring: the loads wait neither for the angles nor for the
+// arithmetic, hold no registers, and each lane waits for its own alone.
 #include "q4.cuh"
 #include "rope.cuh"
 
@@ -22,8 +24,8 @@ namespace gqa {
 namespace {
 
 constexpr int kWarps = 4;              // warps per CTA
-constexpr int kAhead = 5;              // passes loaded ahead
-constexpr int kWantWarps = 148 * 16;   // warps that fill the device
+constexpr int kResident = 5;           // CTAs per SM
+constexpr int kRing = 8;               // passes on their way or waiting, per warp
 
 struct AxisTable {
     uint8_t axis[64];
@@ -39,6 +41,7 @@ struct AppendArgs {
     const int32_t *pos0, *n_tok, *pos;
     int32_t *new_len, *status;
     int B, T, Hq, Hkv, Lmax, n_slices;
+    unsigned units;                    // tokens x slices
     int qk_norm;
     float eps;
 };
@@ -73,12 +76,118 @@ __device__ __forceinline__ void load_gains(float (*gain)[D], const uint16_t *qg,
     }
 }
 
+// The rotation of the lane's 8 pairs (a, b) with the gains folded in:
+//   ya = a (ga c) - b (gb s),   yb = a (ga s) + b (gb c).
+struct Turn {
+    float ac[8], nbs[8], as[8], bc[8];                     // nbs = -gb s
+};
+
+template <int D>
+__device__ __forceinline__ void make_turn(Turn &t, const float *cs, const float *sn,
+                                          const float *gain, int j, bool active) {
+    float c[8], s[8];
+    lane_angles<D>(cs, sn, j, active, c, s);
+#pragma unroll
+    for (int h = 0; h < 8; h += 4) {
+        float4 ga = make_float4(0.f, 0.f, 0.f, 0.f), gb = ga;
+        if (active) {
+            ga = *reinterpret_cast<const float4 *>(gain + 8 * j + h);
+            gb = *reinterpret_cast<const float4 *>(gain + D / 2 + 8 * j + h);
+        }
+        const float a[4] = {ga.x, ga.y, ga.z, ga.w}, b[4] = {gb.x, gb.y, gb.z, gb.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            t.ac[h + e] = a[e] * c[h + e];
+            t.as[h + e] = a[e] * s[h + e];
+            t.bc[h + e] = b[e] * c[h + e];
+            t.nbs[h + e] = -(b[e] * s[h + e]);
+        }
+    }
+}
+
+// RMSNorm (if qk_norm) and rotation of the lane's 16 coordinates; with gains of one the
+// bits of rotate_vector.  Lanes without a vector hold zeros.
+template <int D>
+__device__ __forceinline__ void turn_vector(uint4 &a, uint4 &b, const Turn &t, bool qk_norm,
+                                            float eps) {
+    using S = RopeShape<D>;
+    const uint32_t wa[4] = {a.x, a.y, a.z, a.w}, wb[4] = {b.x, b.y, b.z, b.w};
+    float xa[8], xb[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        xa[2 * e] = bf16lo(wa[e]);
+        xa[2 * e + 1] = bf16hi(wa[e]);
+        xb[2 * e] = bf16lo(wb[e]);
+        xb[2 * e + 1] = bf16hi(wb[e]);
+    }
+    if (qk_norm) {
+        float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+            fma2(s0, s1, xa[e], xa[e + 1], xa[e], xa[e + 1], s0, s1);
+            fma2(s0, s1, xb[e], xb[e + 1], xb[e], xb[e + 1], s0, s1);
+        }
+        const float inv = rsqrtf(group_sum<S::kTPV>(s0 + s1) * (1.0f / D) + eps);
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+            mul2(xa[e], xa[e + 1], xa[e], xa[e + 1], inv, inv);
+            mul2(xb[e], xb[e + 1], xb[e], xb[e + 1], inv, inv);
+        }
+    }
+    uint32_t oa[4], ob[4];
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {
+        float ya0, ya1, yb0, yb1;
+        mul2(ya0, ya1, xb[e], xb[e + 1], t.nbs[e], t.nbs[e + 1]);
+        fma2(ya0, ya1, xa[e], xa[e + 1], t.ac[e], t.ac[e + 1], ya0, ya1);
+        mul2(yb0, yb1, xb[e], xb[e + 1], t.bc[e], t.bc[e + 1]);
+        fma2(yb0, yb1, xa[e], xa[e + 1], t.as[e], t.as[e + 1], yb0, yb1);
+        oa[e / 2] = pack_bf16x2(ya0, ya1);
+        ob[e / 2] = pack_bf16x2(yb0, yb1);
+    }
+    a = make_uint4(oa[0], oa[1], oa[2], oa[3]);
+    b = make_uint4(ob[0], ob[1], ob[2], ob[3]);
+}
+
+// 16 bytes, global to shared; counted by commit groups.
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// A warp's way through its units: unit, unit + stride, .. below units, those whose
+// token is not to be written left out.
+struct Walk {
+    unsigned unit, stride, units;
+    int tok, b, t, slice, slot_row;
+
+    // To the first live unit from `unit` on; false behind the last.
+    __device__ __forceinline__ bool find(const AppendArgs &A) {
+        for (; unit < units; unit += stride) {
+            tok = (int)(unit / (unsigned)A.n_slices);
+            slice = (int)(unit - (unsigned)tok * A.n_slices);
+            b = tok / A.T;
+            t = tok - b * A.T;
+            const int p0 = A.pos0 ? A.pos0[b] : 0;
+            const int n = A.n_tok ? A.n_tok[b] : A.T;
+            slot_row = p0 + t;
+            if (p0 >= 0 && n >= 0 && n <= A.T && (long long)p0 + n <= A.Lmax && t < n) return true;
+        }
+        return false;
+    }
+};
+
 template <int D, bool Q4>
-__global__ void __launch_bounds__(kWarps * 32)
+__global__ void __launch_bounds__(kWarps * 32, kResident)
 norm_rope_append_kernel(const AppendArgs A, const __grid_constant__ RopeTable tab,
                         const __grid_constant__ AxisTable ax) {
     using S = RopeShape<D>;
     using R = Q4Shape<D>;
+    __shared__ __align__(16) uint4 ring[kWarps][kRing][2][32];
     __shared__ __align__(16) float cs[kWarps][S::kHalf];
     __shared__ __align__(16) float sn[kWarps][S::kHalf];
     __shared__ __align__(16) float gain[2][D];
@@ -86,113 +195,131 @@ norm_rope_append_kernel(const AppendArgs A, const __grid_constant__ RopeTable ta
     // of its inputs: wait for that kernel to complete before reading.
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
-    load_gains<D>(gain, A.q_gain, A.k_gain, threadIdx.x, kWarps * 32);
-    __syncthreads();
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const long long unit = (long long)blockIdx.x * kWarps + warp;
-    const int tok = (int)(unit / A.n_slices);
-    const int slice = (int)(unit - (long long)tok * A.n_slices);
-    if (tok >= A.B * A.T) return;                  // only warp-level sync follows
-    const int b = tok / A.T, t = tok - b * A.T;
-    const int p0 = A.pos0 ? A.pos0[b] : 0;
-    const int n = A.n_tok ? A.n_tok[b] : A.T;
-    const bool bad = p0 < 0 || n < 0 || n > A.T;
-    const long long end = (long long)p0 + (bad ? 0 : n);
-    if (t == 0 && slice == 0 && lane == 0) {
+    const int j = lane % S::kTPV;
+    const int slot = lane / S::kTPV;
+    const bool active = j < S::kChunks;
+    // Passes of one kind each: query heads, then key heads, then value heads.
+    const int nq = A.q ? A.Hq : 0;
+    const int qp = (nq + S::kVecPerWarp - 1) / S::kVecPerWarp;
+    const int kp = (A.Hkv + S::kVecPerWarp - 1) / S::kVecPerWarp;
+    const int npass = qp + 2 * kp;
+
+    Walk ahead;                        // of the loads
+    ahead.unit = blockIdx.x * kWarps + warp;
+    ahead.stride = gridDim.x * kWarps;
+    ahead.units = A.units;
+    Walk at = ahead;                   // of the arithmetic
+    const uint32_t mine = static_cast<uint32_t>(__cvta_generic_to_shared(&ring[warp][0][0][lane]));
+    const int step_h = A.n_slices * S::kVecPerWarp;        // heads from pass to pass
+    bool more = ahead.find(A);
+    int ps_ahead = ahead.slice, end_ahead = 0;             // next pass, end of its kind
+    int left_ahead = 0;                                    // heads of its kind from the lane's on
+    const uint16_t *src = nullptr;
+    // Starts the loads of the next pass, into a stage; always one commit group.
+    auto load_next = [&](int stage) {
+        if (more) {                                        // uniform across the warp
+            if (ps_ahead >= end_ahead) {                   // the first pass of a kind
+                const bool is_q = ps_ahead < qp, is_k = !is_q && ps_ahead < qp + kp;
+                end_ahead = is_q ? qp : is_k ? qp + kp : npass;
+                const int h = (ps_ahead - (is_q ? 0 : is_k ? qp : qp + kp)) * S::kVecPerWarp + slot;
+                const int heads = is_q ? A.Hq : A.Hkv;
+                src = (is_q ? A.q : is_k ? A.k : A.v) + ((size_t)ahead.tok * heads + h) * D + 8 * j;
+                left_ahead = active ? heads - h : 0;
+            }
+            if (left_ahead > 0) {
+                copy16(mine + stage * 1024, src);
+                copy16(mine + stage * 1024 + 512, src + S::kHalf);
+            }
+            src += (size_t)step_h * D;
+            left_ahead -= step_h;
+            ps_ahead += A.n_slices;
+            if (ps_ahead >= npass) {
+                ahead.unit += ahead.stride;
+                more = ahead.find(A);
+                ps_ahead = ahead.slice;
+                end_ahead = 0;
+            }
+        }
+        copy_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < kRing - 1; ++i) load_next(i);
+
+    // Lengths and errors of the sequences, by the units of their first tokens.
+    for (unsigned u = blockIdx.x * kWarps + warp; u < A.units; u += gridDim.x * kWarps) {
+        const unsigned tok = u / (unsigned)A.n_slices;
+        if (tok * A.n_slices != u || tok % (unsigned)A.T != 0 || lane != 0) continue;
+        const int b = (int)(tok / (unsigned)A.T);
+        const int p0 = A.pos0 ? A.pos0[b] : 0;
+        const int n = A.n_tok ? A.n_tok[b] : A.T;
+        const bool bad = p0 < 0 || n < 0 || n > A.T;
+        const long long end = (long long)p0 + (n < 0 || n > A.T ? 0 : n);
         if (bad) report(A.status, GQA_DEV_BAD_LEN);
         else if (end > A.Lmax) report(A.status, GQA_DEV_CAPACITY);
         if (A.new_len) A.new_len[b] = (int)(end < 0x7fffffffLL ? end : 0x7fffffffLL);
     }
-    if (bad || end > A.Lmax || t >= n) return;
-    const int slot_row = p0 + t;
+    load_gains<D>(gain, A.q_gain, A.k_gain, threadIdx.x, kWarps * 32);
+    __syncthreads();                                       // only warp-level sync follows
 
-    const int j = lane % S::kTPV;
-    const int slot = lane / S::kTPV;
-    const bool active = j < S::kChunks;
-    const int nq = A.q ? A.Hq : 0, nk = A.Hkv;
-    const int nrot = nq + nk, nvec = nrot + nk;
-    const int npass = (nvec + S::kVecPerWarp - 1) / S::kVecPerWarp;
-
-    auto source = [&](int r) -> const uint16_t * {
-        if (r < nq) return A.q + ((size_t)tok * A.Hq + r) * D;
-        if (r < nrot) return A.k + ((size_t)tok * A.Hkv + (r - nq)) * D;
-        return A.v + ((size_t)tok * A.Hkv + (r - nrot)) * D;
-    };
-
-    float c[8], sv[8];
-    const int step = A.n_slices;
-    for (int pb = slice; pb < npass; pb += step * kAhead) {
-        uint4 ra[kAhead], rb[kAhead];
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-            const int r = (pb + u * step) * S::kVecPerWarp + slot;
-            ra[u] = make_uint4(0, 0, 0, 0);
-            rb[u] = make_uint4(0, 0, 0, 0);
-            if (r < nvec && active) {
-                const uint16_t *src = source(r);
-                ra[u] = *reinterpret_cast<const uint4 *>(src + 8 * j);
-                rb[u] = *reinterpret_cast<const uint4 *>(src + S::kHalf + 8 * j);
+    int stage = 0;
+    for (; at.find(A); at.unit += at.stride) {
+        __syncwarp();                                      // the last unit's angles are read
+        token_angles<D>(cs[warp], sn[warp], A.pos, at.slot_row, A.B, A.T, at.b, at.t, tab, ax,
+                        lane);
+        __syncwarp();
+        Turn turn;
+        int end = 0, left = 0;                             // as of the loads
+        bool is_q = false, is_k = false;
+        uint16_t *dst = nullptr;                           // the lane's first chunk (not Q4's K, V)
+        size_t row = 0;                                    // the cache row
+#pragma unroll 1
+        for (int ps = at.slice; ps < npass; ps += A.n_slices) {
+            if (ps >= end) {                               // the first pass of a kind: uniform
+                is_q = ps < qp;
+                is_k = !is_q && ps < qp + kp;
+                end = is_q ? qp : is_k ? qp + kp : npass;
+                const int h = (ps - (is_q ? 0 : is_k ? qp : qp + kp)) * S::kVecPerWarp + slot;
+                left = active ? (is_q ? A.Hq : A.Hkv) - h : 0;
+                row = ((size_t)at.b * A.Hkv + h) * A.Lmax + at.slot_row;
+                if (is_q) dst = A.q_out + ((size_t)at.tok * A.Hq + h) * D + 8 * j;
+                else if (!Q4) dst = (is_k ? A.kc : A.vc) + row * D + 8 * j;
+                if (is_q || is_k) make_turn<D>(turn, cs[warp], sn[warp], gain[is_k], j, active);
             }
-        }
-        if (pb == slice) {
-            token_angles<D>(cs[warp], sn[warp], A.pos, slot_row, A.B, A.T, b, t, tab, ax, lane);
-            __syncwarp();
-            lane_angles<D>(cs[warp], sn[warp], j, active, c, sv);
-        }
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-            if (pb + u * step >= npass) break;             // uniform across the warp
-            const int r0 = (pb + u * step) * S::kVecPerWarp;
-            const int r = r0 + slot;
-            const bool mem = r < nvec && active;
-            uint4 a = ra[u], bb = rb[u];
-            if (r0 < nrot) {                               // uniform across the warp
-                uint4 oa, ob;
-                rotate_vector<D, true>(a, bb, oa, ob, c, sv, mem, A.qk_norm != 0, A.eps,
-                                       gain[r < nq ? 0 : 1] + 8 * j);
-                if (r < nrot) {
-                    a = oa;
-                    bb = ob;
-                }
+            copy_wait<kRing - 2>();
+            uint4 a = make_uint4(0, 0, 0, 0), bb = a;
+            const bool mem = left > 0;
+            if (mem) {
+                a = ring[warp][stage][0][lane];
+                bb = ring[warp][stage][1][lane];
             }
-            if constexpr (!Q4) {
+            load_next(stage == 0 ? kRing - 1 : stage - 1); // the stage read before this one
+            stage = stage == kRing - 1 ? 0 : stage + 1;
+            if (is_q || is_k) turn_vector<D>(a, bb, turn, A.qk_norm != 0, A.eps);
+            if (!Q4 || is_q) {
                 if (mem) {
-                    uint16_t *dst;
-                    if (r < nq) {
-                        dst = A.q_out + ((size_t)tok * A.Hq + r) * D;
-                    } else {
-                        const int h = r < nrot ? r - nq : r - nrot;
-                        dst = (r < nrot ? A.kc : A.vc) +
-                              (((size_t)b * A.Hkv + h) * A.Lmax + slot_row) * D;
-                    }
-                    *reinterpret_cast<uint4 *>(dst + 8 * j) = a;
-                    *reinterpret_cast<uint4 *>(dst + S::kHalf + 8 * j) = bb;
+                    *reinterpret_cast<uint4 *>(dst) = a;
+                    *reinterpret_cast<uint4 *>(dst + S::kHalf) = bb;
                 }
+                dst += (size_t)step_h * D * (is_q ? 1 : A.Lmax);
             } else {
-                if (mem && r < nq) {
-                    uint16_t *dst = A.q_out + ((size_t)tok * A.Hq + r) * D;
-                    *reinterpret_cast<uint4 *>(dst + 8 * j) = a;
-                    *reinterpret_cast<uint4 *>(dst + S::kHalf + 8 * j) = bb;
+                uint32_t codes[2], sm;
+                q4_quantise(a, bb, codes, sm);
+                if (mem) {
+                    const int g = j >> 1, k0 = 2 * (j & 1);
+                    uint32_t *cw = reinterpret_cast<uint32_t *>(is_k ? A.k_codes : A.v_codes) +
+                                   row * (R::kCodeBytes / 4);
+                    cw[R::NG * k0 + g] = codes[0];
+                    cw[R::NG * (k0 + 1) + g] = codes[1];
+                    if ((j & 1) == 0) (is_k ? A.k_scales : A.v_scales)[row * R::NG + g] = sm;
                 }
-                if (r0 + S::kVecPerWarp > nq) {            // uniform: some vector is K or V
-                    uint32_t codes[2], sm;
-                    q4_quantise(a, bb, codes, sm);
-                    if (mem && r >= nq) {
-                        const int h = r < nrot ? r - nq : r - nrot;
-                        const size_t row = ((size_t)b * A.Hkv + h) * A.Lmax + slot_row;
-                        const int g = j >> 1, k0 = 2 * (j & 1);
-                        uint32_t *cw = reinterpret_cast<uint32_t *>(r < nrot ? A.k_codes
-                                                                             : A.v_codes) +
-                                       row * (R::kCodeBytes / 4);
-                        cw[R::NG * k0 + g] = codes[0];
-                        cw[R::NG * (k0 + 1) + g] = codes[1];
-                        if ((j & 1) == 0) (r < nrot ? A.k_scales : A.v_scales)[row * R::NG + g] = sm;
-                    }
-                }
+                row += (size_t)step_h * A.Lmax;
             }
+            left -= step_h;
         }
     }
+    copy_wait<0>();
 }
 
 // ---------------------------------------------------------------------------
@@ -204,45 +331,49 @@ norm_rope_append_kernel(const AppendArgs A, const __grid_constant__ RopeTable ta
 //   dx = r z - x r^3 mean(x z)          (without the norm: dx = w),
 // and dv is the cache's gradient rows brought back to token order.
 //
-// Bound by memory: x, dy read once and dx written once.  Warps take (token, slice)
-// units as in the forward, a fixed number of them in turn, and keep the sums of
-// d gain for their lanes' 16 coordinates in registers over all their units; a CTA
-// adds its warps' sums and leaves one row per CTA in the workspace, and a second
-// kernel adds the rows in a fixed order, so equal calls give equal bits.
-constexpr int kBwdWarps = 8;
-constexpr int kBwdMaxCtas = 2 * 148;   // two CTAs per SM
-constexpr int kBwdAhead = 2;           // passes loaded ahead (two vectors each)
+// Bound by memory: x, dy read once and dx written once.  The loads go through rings as
+// in the forward.  A CTA takes either query passes or key and value passes, of tokens
+// (or slices of them) in turn, so that a lane keeps one gain and the sums of one gain's
+// gradient, for its 16 coordinates, in registers over all its units; the CTAs are
+// shared out by the bytes of the two.  At the end a CTA adds its warps' sums and leaves
+// one row in the workspace, and a second kernel adds the rows in a fixed order, so
+// equal calls give equal bits.
+constexpr int kBwdWarps = 4;
+constexpr int kBwdResident = 3;                            // CTAs per SM
+constexpr int kBwdMaxCtas = 148 * kBwdResident;
+constexpr int kBwdRing = 5;                                // passes on their way or waiting
 
 struct BackwardArgs {
     const uint16_t *q, *k, *dq_out, *dkc, *dvc;
     uint16_t *dq, *dk, *dv;
     const uint16_t *q_gain, *k_gain;
     const int32_t *pos0, *pos;
-    float *partial;                    // [CTAs][2][D], NULL: no gain gradients wanted
+    float *partial;                    // [CTAs][D], NULL: no gain gradients wanted
     int32_t *status;
-    int B, T, Hq, Hkv, Lmax, n_slices;
+    int B, T, Hq, Hkv, Lmax;
+    int n_q;                           // CTAs of the query passes; the rest: keys and values
+    int slices[2];                     // slices of a token's passes: query, key and value
+    unsigned units[2];                 // tokens x slices
     int qk_norm;
     float eps;
 };
 
-// One vector: dx of the lane's 16 coordinates, and its share of d gain added to dg.
+// One vector: dx of the lane's 16 coordinates in place of dy (ya, yb), and its share of
+// d gain added to dg.  Lanes without a vector hold zeros.
 template <int D>
-__device__ __forceinline__ void backward_vector(const uint4 xa_in, const uint4 xb_in,
-                                                const uint4 ya_in, const uint4 yb_in, uint4 &da,
-                                                uint4 &db, const float (&c)[8],
-                                                const float (&sv)[8], bool live, bool qk_norm,
-                                                float eps, const float *gain, float (&dg)[16]) {
+__device__ __forceinline__ void backward_vector(const uint4 xa, const uint4 xb, uint4 &ya,
+                                                uint4 &yb, const float (&c)[8],
+                                                const float (&s)[8], bool qk_norm, float eps,
+                                                const float (&gain)[16], float (&dg)[16]) {
     using S = RopeShape<D>;
-    const uint32_t xw[8] = {xa_in.x, xa_in.y, xa_in.z, xa_in.w,
-                            xb_in.x, xb_in.y, xb_in.z, xb_in.w};
-    const uint32_t yw[8] = {ya_in.x, ya_in.y, ya_in.z, ya_in.w,
-                            yb_in.x, yb_in.y, yb_in.z, yb_in.w};
+    const uint32_t xw[8] = {xa.x, xa.y, xa.z, xa.w, xb.x, xb.y, xb.z, xb.w};
+    const uint32_t yw[8] = {ya.x, ya.y, ya.z, ya.w, yb.x, yb.y, yb.z, yb.w};
     float w[16];                       // [0..7] first-half chunk, [8..15] second-half chunk
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         const float a0 = bf16lo(yw[e]), a1 = bf16hi(yw[e]);
         const float b0 = bf16lo(yw[4 + e]), b1 = bf16hi(yw[4 + e]);
-        const float c0 = c[2 * e], c1 = c[2 * e + 1], s0 = sv[2 * e], s1 = sv[2 * e + 1];
+        const float c0 = c[2 * e], c1 = c[2 * e + 1], s0 = s[2 * e], s1 = s[2 * e + 1];
         mul2(w[2 * e], w[2 * e + 1], b0, b1, s0, s1);
         fma2(w[2 * e], w[2 * e + 1], a0, a1, c0, c1, w[2 * e], w[2 * e + 1]);
         mul2(w[8 + 2 * e], w[9 + 2 * e], a0, a1, -s0, -s1);
@@ -250,186 +381,239 @@ __device__ __forceinline__ void backward_vector(const uint4 xa_in, const uint4 x
     }
     if (qk_norm) {                     // uniform
         float ss0 = 0.f, ss1 = 0.f, xz0 = 0.f, xz1 = 0.f;
-        float z[16];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float x0 = bf16lo(xw[e]), x1 = bf16hi(xw[e]);
-            float g0 = 0.f, g1 = 0.f;
-            if (live) {
-                const float2 gg = *reinterpret_cast<const float2 *>(
-                    gain + (e < 4 ? 2 * e : S::kHalf + 2 * (e - 4)));
-                g0 = gg.x;
-                g1 = gg.y;
-            }
+        for (int e = 0; e < 16; e += 2) {
+            const float x0 = bf16lo(xw[e / 2]), x1 = bf16hi(xw[e / 2]);
+            float z0, z1;
             fma2(ss0, ss1, x0, x1, x0, x1, ss0, ss1);
-            mul2(z[2 * e], z[2 * e + 1], w[2 * e], w[2 * e + 1], g0, g1);
-            fma2(xz0, xz1, x0, x1, z[2 * e], z[2 * e + 1], xz0, xz1);
+            mul2(z0, z1, w[e], w[e + 1], gain[e], gain[e + 1]);
+            fma2(xz0, xz1, x0, x1, z0, z1, xz0, xz1);
         }
-        const float ss = group_sum<S::kTPV>(ss0 + ss1);      // lanes not live hold zeros
+        const float ss = group_sum<S::kTPV>(ss0 + ss1);
         const float xz = group_sum<S::kTPV>(xz0 + xz1);
-        const float r = live ? rsqrtf(ss * (1.0f / D) + eps) : 0.f;
-        const float k = -r * (xz * r * (1.0f / D));          // r^3 alone could overflow
+        const float r = rsqrtf(ss * (1.0f / D) + eps);
+        const float k = -r * (xz * r * (1.0f / D));        // r^3 alone could overflow
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float x0 = bf16lo(xw[e]), x1 = bf16hi(xw[e]);
-            float t0, t1;
-            mul2(t0, t1, x0, x1, r, r);
-            fma2(dg[2 * e], dg[2 * e + 1], w[2 * e], w[2 * e + 1], t0, t1, dg[2 * e],
-                 dg[2 * e + 1]);
+        for (int e = 0; e < 16; e += 2) {
+            float t0, t1, z0, z1;
+            mul2(t0, t1, bf16lo(xw[e / 2]), bf16hi(xw[e / 2]), r, r);
+            fma2(dg[e], dg[e + 1], w[e], w[e + 1], t0, t1, dg[e], dg[e + 1]);
+            mul2(z0, z1, w[e], w[e + 1], gain[e], gain[e + 1]);
             mul2(t0, t1, t0, t1, k, k);
-            fma2(w[2 * e], w[2 * e + 1], z[2 * e], z[2 * e + 1], r, r, t0, t1);
+            fma2(w[e], w[e + 1], z0, z1, r, r, t0, t1);
         }
     }
     uint32_t o[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) o[e] = pack_bf16x2(w[2 * e], w[2 * e + 1]);
-    da = make_uint4(o[0], o[1], o[2], o[3]);
-    db = make_uint4(o[4], o[5], o[6], o[7]);
+    ya = make_uint4(o[0], o[1], o[2], o[3]);
+    yb = make_uint4(o[4], o[5], o[6], o[7]);
 }
 
 template <int D>
-__global__ void __launch_bounds__(kBwdWarps * 32, 2)
-norm_rope_backward_kernel(const BackwardArgs A, const __grid_constant__ RopeTable tab,
-                          const __grid_constant__ AxisTable ax) {
-    using S = RopeShape<D>;
-    __shared__ __align__(16) float cs[kBwdWarps][S::kHalf];
-    __shared__ __align__(16) float sn[kBwdWarps][S::kHalf];
-    __shared__ __align__(16) float gain[2][D];
-    __shared__ __align__(16) float sums[kBwdWarps][2][D];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;");
-    load_gains<D>(gain, A.q_gain, A.k_gain, threadIdx.x, kBwdWarps * 32);
-    __syncthreads();
+struct BackwardShared {
+    uint4 ring[kBwdWarps][kBwdRing][4][32];                // dy, dy, x, x
+    float cs[kBwdWarps][D / 2], sn[kBwdWarps][D / 2];
+    float sums[kBwdWarps][D];
+};
 
+// The warp's units: query passes (QUERIES) or key passes, then value passes.
+template <int D, bool QUERIES>
+__device__ __forceinline__ void backward_units(const BackwardArgs &A, const RopeTable &tab,
+                                               const AxisTable &ax, BackwardShared<D> &sh) {
+    using S = RopeShape<D>;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int j = lane % S::kTPV, slot = lane / S::kTPV;
     const bool active = j < S::kChunks;
-    // Passes of one kind each: query heads, then key heads, then value heads.
-    const int qp = (A.Hq + S::kVecPerWarp - 1) / S::kVecPerWarp;
-    const int kp = (A.Hkv + S::kVecPerWarp - 1) / S::kVecPerWarp;
-    const int npass = qp + 2 * kp;
-    float dgq[16], dgk[16];
-#pragma unroll
-    for (int e = 0; e < 16; ++e) dgq[e] = dgk[e] = 0.f;
+    const int heads = QUERIES ? A.Hq : A.Hkv;
+    const int per_kind = (heads + S::kVecPerWarp - 1) / S::kVecPerWarp;
+    const int npass = QUERIES ? per_kind : 2 * per_kind;
+    const unsigned n_slices = A.slices[QUERIES ? 0 : 1], units = A.units[QUERIES ? 0 : 1];
+    const int cta = QUERIES ? (int)blockIdx.x : (int)blockIdx.x - A.n_q;
+    const unsigned stride = (QUERIES ? A.n_q : gridDim.x - A.n_q) * kBwdWarps;
+    const bool norm = A.qk_norm != 0;
 
-    const long long units = (long long)A.B * A.T * A.n_slices;
-    const long long stride = (long long)gridDim.x * kBwdWarps;
-    for (long long unit = (long long)blockIdx.x * kBwdWarps + warp; unit < units;
-         unit += stride) {
-        const int tok = (int)(unit / A.n_slices);
-        const int slice = (int)(unit - (long long)tok * A.n_slices);
-        const int b = tok / A.T, t = tok - b * A.T;
-        const int p0 = A.pos0 ? A.pos0[b] : 0;
-        if (p0 < 0 || (long long)p0 + A.T > A.Lmax) {
-            if (t == 0 && slice == 0 && lane == 0)
-                report(A.status, p0 < 0 ? GQA_DEV_BAD_LEN : GQA_DEV_CAPACITY);
-            continue;
-        }
-        const int slot_row = p0 + t;
-        float c[8], sv[8];
-        for (int pb = slice; pb < npass; pb += A.n_slices * kBwdAhead) {
-            uint4 x[kBwdAhead][2], y[kBwdAhead][2];
-#pragma unroll
-            for (int u = 0; u < kBwdAhead; ++u) {
-                const int ps = pb + u * A.n_slices;
-                const bool is_q = ps < qp, is_k = !is_q && ps < qp + kp;
-                const int h = (is_q ? ps : is_k ? ps - qp : ps - qp - kp) * S::kVecPerWarp + slot;
-                x[u][0] = x[u][1] = y[u][0] = y[u][1] = make_uint4(0, 0, 0, 0);
-                if (ps < npass && active && h < (is_q ? A.Hq : A.Hkv)) {
-                    const size_t in = is_q ? ((size_t)tok * A.Hq + h) * D
-                                           : ((size_t)tok * A.Hkv + h) * D;
-                    const size_t row = (((size_t)b * A.Hkv + h) * A.Lmax + slot_row) * D;
-                    const uint16_t *ys = is_q ? A.dq_out + in : (is_k ? A.dkc : A.dvc) + row;
-                    y[u][0] = *reinterpret_cast<const uint4 *>(ys + 8 * j);
-                    y[u][1] = *reinterpret_cast<const uint4 *>(ys + S::kHalf + 8 * j);
-                    if ((is_q || is_k) && A.qk_norm) {
-                        const uint16_t *xs = (is_q ? A.q : A.k) + in;
-                        x[u][0] = *reinterpret_cast<const uint4 *>(xs + 8 * j);
-                        x[u][1] = *reinterpret_cast<const uint4 *>(xs + S::kHalf + 8 * j);
-                    }
-                }
-            }
-            if (pb == slice) {
-                __syncwarp();          // the warp's last unit has read its angles
-                token_angles<D>(cs[warp], sn[warp], A.pos, slot_row, A.B, A.T, b, t, tab, ax,
-                                lane);
-                __syncwarp();
-                lane_angles<D>(cs[warp], sn[warp], j, active, c, sv);
-            }
-#pragma unroll
-            for (int u = 0; u < kBwdAhead; ++u) {
-                const int ps = pb + u * A.n_slices;
-                if (ps >= npass) break;                    // uniform across the warp
-                const bool is_q = ps < qp, is_k = !is_q && ps < qp + kp;
-                const int h = (is_q ? ps : is_k ? ps - qp : ps - qp - kp) * S::kVecPerWarp + slot;
-                const bool live = active && h < (is_q ? A.Hq : A.Hkv);
-                uint4 da = y[u][0], db = y[u][1];
-                if (is_q)
-                    backward_vector<D>(x[u][0], x[u][1], y[u][0], y[u][1], da, db, c, sv, live,
-                                       A.qk_norm != 0, A.eps, gain[0] + 8 * j, dgq);
-                else if (is_k)
-                    backward_vector<D>(x[u][0], x[u][1], y[u][0], y[u][1], da, db, c, sv, live,
-                                       A.qk_norm != 0, A.eps, gain[1] + 8 * j, dgk);
-                if (live) {
-                    uint16_t *dst = is_q ? A.dq + ((size_t)tok * A.Hq + h) * D
-                                         : (is_k ? A.dk : A.dv) + ((size_t)tok * A.Hkv + h) * D;
-                    *reinterpret_cast<uint4 *>(dst + 8 * j) = da;
-                    *reinterpret_cast<uint4 *>(dst + S::kHalf + 8 * j) = db;
-                }
-            }
-        }
-    }
-    if (!A.partial) return;            // uniform over the grid
-    // The lanes of a warp that hold the same coordinates, then the CTA's warps.
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-#pragma unroll
-        for (int o = S::kTPV; o < 32; o <<= 1) {
-            dgq[e] += __shfl_xor_sync(0xffffffffu, dgq[e], o);
-            dgk[e] += __shfl_xor_sync(0xffffffffu, dgk[e], o);
-        }
-    }
-    if (slot == 0 && active) {
+    float gain[16], dg[16];
+    {
+        const uint16_t *g = QUERIES ? A.q_gain : A.k_gain;
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
             const int d = (e < 8 ? 0 : S::kHalf) + 8 * j + (e & 7);
-            sums[warp][0][d] = dgq[e];
-            sums[warp][1][d] = dgk[e];
+            gain[e] = !active ? 0.f : g ? __uint_as_float((uint32_t)g[d] << 16) : 1.0f;
+            dg[e] = 0.f;
         }
     }
-    __syncthreads();
-    for (int i = threadIdx.x; i < 2 * D; i += kBwdWarps * 32) {
-        float s = 0.f;
+
+    // Unit u: its token, sequence, cache slot and slice; the first in range from u on.
+    auto find = [&](unsigned u, unsigned &tok, unsigned &b, int &slot_row, int &slice) {
+        for (; u < units; u += stride) {
+            tok = u / n_slices;
+            b = tok / (unsigned)A.T;
+            const int p0 = A.pos0 ? A.pos0[b] : 0;
+            slot_row = p0 + (int)(tok - b * A.T);
+            slice = (int)(u - tok * n_slices);
+            if (p0 >= 0 && (long long)p0 + A.T <= A.Lmax) break;
+        }
+        return u;
+    };
+    const int step_h = (int)n_slices * S::kVecPerWarp;     // heads from pass to pass
+    const size_t x_step = (size_t)step_h * D, y_step = QUERIES ? x_step : x_step * A.Lmax;
+
+    // The loads, kBwdRing - 1 passes ahead of the arithmetic.
+    unsigned tok = 0, b = 0;
+    int slot_row = 0, kps = 0, kend = 0, kleft = 0;
+    unsigned ku = find(cta * kBwdWarps + warp, tok, b, slot_row, kps);
+    const uint16_t *xs = nullptr, *ys = nullptr;
+    const uint32_t mine =
+        static_cast<uint32_t>(__cvta_generic_to_shared(&sh.ring[warp][0][0][lane]));
+    auto load_next = [&](int stage) {
+        if (ku < units) {                                  // uniform across the warp
+            const bool value = !QUERIES && kps >= per_kind;
+            if (kps >= kend) {                             // the first pass of a kind
+                kend = value ? npass : per_kind;
+                const int h = (value ? kps - per_kind : kps) * S::kVecPerWarp + slot;
+                const size_t in = ((size_t)tok * heads + h) * D + 8 * j;
+                const size_t row = (((size_t)b * A.Hkv + h) * A.Lmax + slot_row) * D + 8 * j;
+                xs = (QUERIES ? A.q : A.k) + in;
+                ys = QUERIES ? A.dq_out + in : (value ? A.dvc : A.dkc) + row;
+                kleft = active ? heads - h : 0;
+            }
+            if (kleft > 0) {
+                const uint32_t dst = mine + stage * 2048;
+                copy16(dst, ys);
+                copy16(dst + 512, ys + S::kHalf);
+                if (norm && !value) {
+                    copy16(dst + 1024, xs);
+                    copy16(dst + 1536, xs + S::kHalf);
+                }
+            }
+            xs += x_step;
+            ys += y_step;
+            kleft -= step_h;
+            kps += n_slices;
+            if (kps >= npass) {
+                ku = find(ku + stride, tok, b, slot_row, kps);
+                kend = 0;
+            }
+        }
+        copy_commit();
+    };
 #pragma unroll
-        for (int w = 0; w < kBwdWarps; ++w) s += sums[w][i / D][i % D];
-        A.partial[(size_t)blockIdx.x * 2 * D + i] = s;
+    for (int i = 0; i < kBwdRing - 1; ++i) load_next(i);
+
+    int stage = 0;
+    unsigned at_tok = 0, at_b = 0;
+    int at_row = 0, ps = 0;
+#pragma unroll 1
+    for (unsigned u = cta * kBwdWarps + warp;
+         (u = find(u, at_tok, at_b, at_row, ps)) < units; u += stride) {
+        __syncwarp();                                      // the warp's last unit has read its angles
+        token_angles<D>(sh.cs[warp], sh.sn[warp], A.pos, at_row, A.B, A.T, (int)at_b,
+                        (int)(at_tok - at_b * A.T), tab, ax, lane);
+        __syncwarp();
+        float c[8], s[8];
+        lane_angles<D>(sh.cs[warp], sh.sn[warp], j, active, c, s);
+        int end = 0, left = 0;
+        uint16_t *dst = nullptr;
+#pragma unroll 1
+        for (; ps < npass; ps += n_slices) {
+            const bool value = !QUERIES && ps >= per_kind; // uniform
+            if (ps >= end) {
+                end = value ? npass : per_kind;
+                const int h = (value ? ps - per_kind : ps) * S::kVecPerWarp + slot;
+                dst = (QUERIES ? A.dq : value ? A.dv : A.dk) +
+                      ((size_t)at_tok * heads + h) * D + 8 * j;
+                left = active ? heads - h : 0;
+            }
+            copy_wait<kBwdRing - 2>();
+            const uint4 *place = &sh.ring[warp][stage][0][lane];
+            uint4 ya = make_uint4(0, 0, 0, 0), yb = ya, xa = ya, xb = ya;
+            if (left > 0) {
+                ya = place[0];
+                yb = place[32];
+                if (norm && !value) {
+                    xa = place[64];
+                    xb = place[96];
+                }
+            }
+            load_next(stage == 0 ? kBwdRing - 1 : stage - 1);
+            stage = stage == kBwdRing - 1 ? 0 : stage + 1;
+            if (!value) backward_vector<D>(xa, xb, ya, yb, c, s, norm, A.eps, gain, dg);
+            if (left > 0) {
+                *reinterpret_cast<uint4 *>(dst) = ya;
+                *reinterpret_cast<uint4 *>(dst + S::kHalf) = yb;
+            }
+            dst += x_step;
+            left -= step_h;
+        }
+    }
+    copy_wait<0>();
+    if (!A.partial) return;            // uniform over the grid
+    // The lanes of a warp that hold the same coordinates.
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+#pragma unroll
+        for (int x = S::kTPV; x < 32; x <<= 1) dg[e] += __shfl_xor_sync(0xffffffffu, dg[e], x);
+    if (slot == 0 && active) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) sh.sums[warp][(e < 8 ? 0 : S::kHalf) + 8 * j + (e & 7)] = dg[e];
     }
 }
 
-// d gain = the sum of the CTAs' rows: a CTA per 32 of the 2 D columns, 32 rows at a
-// time, added in the order of the rows.
+template <int D>
+__global__ void __launch_bounds__(kBwdWarps * 32, kBwdResident)
+norm_rope_backward_kernel(const BackwardArgs A, const __grid_constant__ RopeTable tab,
+                          const __grid_constant__ AxisTable ax) {
+    __shared__ __align__(16) BackwardShared<D> sh;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
+    // Errors of the sequences.
+    for (int b = blockIdx.x * kBwdWarps * 32 + threadIdx.x; b < A.B;
+         b += gridDim.x * kBwdWarps * 32) {
+        const int p0 = A.pos0 ? A.pos0[b] : 0;
+        if (p0 < 0 || (long long)p0 + A.T > A.Lmax)
+            report(A.status, p0 < 0 ? GQA_DEV_BAD_LEN : GQA_DEV_CAPACITY);
+    }
+    if ((int)blockIdx.x < A.n_q)                           // the CTA's role
+        backward_units<D, true>(A, tab, ax, sh);
+    else
+        backward_units<D, false>(A, tab, ax, sh);
+    if (!A.partial) return;
+    __syncthreads();
+    for (int i = threadIdx.x; i < D; i += kBwdWarps * 32) {
+        float x = 0.f;
+#pragma unroll
+        for (int w = 0; w < kBwdWarps; ++w) x += sh.sums[w][i];
+        A.partial[(size_t)blockIdx.x * D + i] = x;
+    }
+}
+
+// d gain = the sum of the CTAs' rows (the first n_q: q's, the others: k's): a CTA per 32
+// columns of either, 32 rows at a time, added in the order of the rows.
 __global__ void __launch_bounds__(1024)
-gain_sum_kernel(const float *__restrict__ partial, int n_rows, int D, float *dq_gain,
+gain_sum_kernel(const float *__restrict__ partial, int n_q, int n_rows, int D, float *dq_gain,
                 float *dk_gain) {
     __shared__ float s[32][33];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int col = blockIdx.x * 32 + (threadIdx.x & 31), r0 = threadIdx.x >> 5;
+    float *dst = blockIdx.y == 0 ? dq_gain : dk_gain;
+    if (!dst) return;
+    const int first = blockIdx.y == 0 ? 0 : n_q, last = blockIdx.y == 0 ? n_q : n_rows;
     float a = 0.f;
-    for (int r = r0; r < n_rows; r += 32) a += partial[(size_t)r * 2 * D + col];
+    for (int r = first + r0; r < last; r += 32) a += partial[(size_t)r * D + col];
     s[r0][threadIdx.x & 31] = a;
     __syncthreads();
     if (r0 == 0) {
         a = 0.f;
 #pragma unroll
         for (int i = 0; i < 32; ++i) a += s[i][threadIdx.x];
-        float *dst = col < D ? dq_gain : dk_gain;
-        if (dst) dst[col < D ? col : col - D] = a;
+        dst[col] = a;
     }
 }
 
 // Slices of a token's passes: one, unless the tokens alone leave most warps idle.
-int slices(long long tokens, int npass) {
-    const long long want = (kWantWarps + tokens - 1) / tokens;
+int slices(long long tokens, int npass, int warps) {
+    const long long want = (warps + tokens - 1) / tokens;
     return (int)(want < 1 ? 1 : want > npass ? npass : want);
 }
 
@@ -445,10 +629,14 @@ cudaError_t launch_append(AppendArgs A, const gqa_rope_params &p, const gqa_rope
                           cudaStream_t s) {
     const long long tokens = (long long)A.B * A.T;
     const int per_pass = RopeShape<D>::kVecPerWarp;
-    A.n_slices = slices(tokens, ((A.q ? A.Hq : 0) + 2 * A.Hkv + per_pass - 1) / per_pass);
-    const long long ctas = (tokens * A.n_slices + kWarps - 1) / kWarps;
-    return launch_pdl(norm_rope_append_kernel<D, Q4>, (unsigned)ctas, kWarps * 32, s, A,
-                      make_table(D, p), axis_table(x));
+    const int npass = ((A.q ? A.Hq : 0) + per_pass - 1) / per_pass +
+                      2 * ((A.Hkv + per_pass - 1) / per_pass);
+    constexpr int kCtas = 148 * kResident;
+    A.n_slices = slices(tokens, npass, kCtas * kWarps);
+    A.units = (unsigned)(tokens * A.n_slices);
+    const unsigned ctas = (A.units + kWarps - 1) / kWarps;
+    return launch_pdl(norm_rope_append_kernel<D, Q4>, ctas < kCtas ? ctas : kCtas, kWarps * 32, s,
+                      A, make_table(D, p), axis_table(x));
 }
 
 template <int D>
@@ -456,15 +644,27 @@ cudaError_t launch_backward(BackwardArgs A, const gqa_rope_params &p, const gqa_
                             float *dq_gain, float *dk_gain, cudaStream_t s) {
     const long long tokens = (long long)A.B * A.T;
     const int per_pass = RopeShape<D>::kVecPerWarp;
-    A.n_slices = slices(tokens, (A.Hq + per_pass - 1) / per_pass +
-                                    2 * ((A.Hkv + per_pass - 1) / per_pass));
-    const long long ctas = (tokens * A.n_slices + kBwdWarps - 1) / kBwdWarps;
-    const unsigned grid = (unsigned)(ctas < kBwdMaxCtas ? ctas : kBwdMaxCtas);
-    cudaError_t e = launch_pdl(norm_rope_backward_kernel<D>, grid, kBwdWarps * 32, s, A,
-                               make_table(D, p), axis_table(x));
+    const int npass[2] = {(A.Hq + per_pass - 1) / per_pass,
+                          2 * ((A.Hkv + per_pass - 1) / per_pass)};
+    // CTAs by the rows moved: three per query and key head, two per value head.
+    const double share = 3.0 * A.Hq / (3.0 * A.Hq + 5.0 * A.Hkv);
+    int most[2], ctas[2];
+    most[0] = (int)(kBwdMaxCtas * share + 0.5);
+    most[0] = most[0] < 1 ? 1 : most[0] > kBwdMaxCtas - 1 ? kBwdMaxCtas - 1 : most[0];
+    most[1] = kBwdMaxCtas - most[0];
+    for (int i = 0; i < 2; ++i) {
+        A.slices[i] = slices(tokens, npass[i], most[i] * kBwdWarps);
+        A.units[i] = (unsigned)(tokens * A.slices[i]);
+        const long long need = ((long long)A.units[i] + kBwdWarps - 1) / kBwdWarps;
+        ctas[i] = (int)(need < most[i] ? need : most[i]);
+    }
+    A.n_q = ctas[0];
+    const int grid = ctas[0] + ctas[1];
+    cudaError_t e = launch_pdl(norm_rope_backward_kernel<D>, dim3((unsigned)grid), kBwdWarps * 32,
+                               s, A, make_table(D, p), axis_table(x));
     if (e != cudaSuccess || !A.partial) return e;
-    return launch_pdl(gain_sum_kernel, 2 * D / 32, 1024, s, (const float *)A.partial, (int)grid,
-                      D, dq_gain, dk_gain);
+    return launch_pdl(gain_sum_kernel, dim3(D / 32, 2), 1024, s, (const float *)A.partial, A.n_q,
+                      grid, D, dq_gain, dk_gain);
 }
 
 bool inputs_ok(const gqa_rope_inputs *x, const gqa_rope_params &p, int D) {
@@ -591,7 +791,7 @@ extern "C" gqa_status gqa_norm_rope_append_q4(const void *q, const void *k, cons
 }
 
 extern "C" size_t gqa_norm_rope_backward_workspace_bytes(int D) {
-    return gqa_host::head_dim_ok(D) ? (size_t)gqa::kBwdMaxCtas * 2 * D * 4 : 0;
+    return gqa_host::head_dim_ok(D) ? (size_t)gqa::kBwdMaxCtas * D * 4 : 0;
 }
 
 extern "C" gqa_status gqa_norm_rope_append_backward(

@@ -186,12 +186,12 @@ inline const RopeTable &make_table(int D, const gqa_rope_params &p) {
 // A launch as a programmatic dependent of the preceding kernel on the stream: its
 // launch overlaps that kernel's last CTAs (the kernel waits for it on entry).
 template <typename K, typename... Args>
-cudaError_t launch_pdl(K kern, unsigned grid, unsigned block, cudaStream_t s, Args... args) {
+cudaError_t launch_pdl(K kern, dim3 grid, unsigned block, cudaStream_t s, Args... args) {
     cudaLaunchAttribute pdl[1];
     pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     pdl[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
+    cfg.gridDim = grid;
     cfg.blockDim = dim3(block);
     cfg.stream = s;
     cfg.attrs = pdl;

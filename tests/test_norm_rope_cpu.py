@@ -172,8 +172,9 @@ def test_workspace_sizes(lib):
     assert f(0, 4, 2, 64, 100) == 0 and f(1, 5, 2, 64, 100) == 0 and f(1, 4, 2, 80, 100) == 0
     assert f(1, 4, 2, 64, 0) == 0
     assert f(1, 4, 2, 64, 1) == 16             # one chunk: no partials
-    # whatever the cut, at least one row of D + 2 floats per 256 slots
-    assert f(64, 24, 8, 128, 2049) >= 64 * 24 * 9 * 130 * 4
+    # whatever the cut: one to max_len / 64 rows of D + 2 floats per query head
+    row = 64 * 24 * 130 * 4
+    assert 2 * row <= f(64, 24, 8, 128, 2049) <= 33 * row + 16
 
 
 # ---------------------------------------------------------------------------
