@@ -17,7 +17,7 @@ import torch
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libgqa.so")
 _lib = None
-_fast_pointers = None                  # csrc/fastargs.c, set by load()
+_fast = _fast_pointers = None          # csrc/fastargs.c, set by load()
 
 GQA_OK = 0
 GQA_DEV_CAPACITY = 0x1
@@ -90,20 +90,20 @@ class Q4Cache:
     scales bf16 [B, Hkv, Lmax, D/32, 2] of K and of V.  :meth:`zeros` makes one."""
 
     def __init__(self, k_codes, k_scales, v_codes, v_scales):
-        if not isinstance(k_codes, torch.Tensor):
-            raise TypeError("k_codes must be a torch.Tensor")
-        if k_codes.dim() != 4 or k_codes.shape[3] not in (32, 48, 64):
-            raise ValueError("k_codes must be [B, Hkv, Lmax, D/2] with D 64, 96 or 128, got %s" %
-                             (tuple(k_codes.shape),))
-        B, Hkv, Lmax, half = self._codes_shape = tuple(k_codes.shape)
-        self.device, self.shape = k_codes.device, (B, Hkv, Lmax, 2 * half)
-        self._scales_shape = (B, Hkv, Lmax, half // 16, 2)
         self.k_codes, self.k_scales = k_codes, k_scales
         self.v_codes, self.v_scales = v_codes, v_scales
-        for part in (k_codes, k_scales, v_codes, v_scales):
-            if part is None:
-                raise TypeError("a Q4Cache needs its four tensors")
-        _pointers(self.device, self._spec())
+        if _fast is None:
+            load()
+        self.shape = _fast.cache(k_codes, k_scales, v_codes, v_scales)
+        if self.shape is None:             # say which of them does not fit
+            for name, part in zip(("k_codes", "k_scales", "v_codes", "v_scales"), self._parts()):
+                _need_tensor(part, name)
+            if k_codes.dim() != 4 or k_codes.shape[3] not in (32, 48, 64):
+                raise ValueError("k_codes must be [B, Hkv, Lmax, D/2] with D 64, 96 or 128, "
+                                 "got %s" % (tuple(k_codes.shape),))
+            self.shape = tuple(k_codes.shape[:3]) + (2 * k_codes.shape[3],)
+            _pointers(k_codes.device, self._spec())
+        self.device = k_codes.device
 
     @classmethod
     def zeros(cls, B, Hkv, Lmax, D, device="cuda"):
@@ -113,9 +113,13 @@ class Q4Cache:
                   for _ in range(2)]
         return cls(codes[0], scales[0], codes[1], scales[1])
 
+    def _parts(self):
+        return self.k_codes, self.k_scales, self.v_codes, self.v_scales
+
     def _spec(self):
         """The cache's part of a call's tensors, for _pointers."""
-        codes, scales = self._codes_shape, self._scales_shape
+        B, Hkv, Lmax, D = self.shape
+        codes, scales = (B, Hkv, Lmax, D // 2), (B, Hkv, Lmax, D // 32, 2)
         return ("k_codes", self.k_codes, torch.uint8, codes,
                 "k_scales", self.k_scales, torch.bfloat16, scales,
                 "v_codes", self.v_codes, torch.uint8, codes,
@@ -165,7 +169,7 @@ class GqaError(RuntimeError):
 
 def load(path: str | None = None):
     """Load libgqa.so (raises if it is missing: there is no fallback)."""
-    global _lib, _fast_pointers
+    global _lib, _fast, _fast_pointers
     if _lib is None:
         p = path or LIB_PATH
         if not os.path.exists(p):
@@ -184,7 +188,10 @@ def load(path: str | None = None):
         _fastargs.setup(torch.Tensor.__dlpack_c_exchange_api__, (
             (torch.bfloat16, 4, 16), (torch.int32, 0, 32), (torch.uint8, 1, 8),
             (torch.float32, 2, 32)))
-        _fast_pointers = _fastargs.pointers
+        _fastargs.entries(tuple(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
+            "gqa_norm_rope_append", "gqa_norm_rope_append_q4", "gqa_norm_rope_append_backward",
+            "kv_cache_read_q4", "gqa_decode_q4")))
+        _fast, _fast_pointers = _fastargs, _fastargs.pointers
         _lib = lib
     return _lib
 
@@ -278,6 +285,20 @@ def _launch(name, dev, stream, current, *args):
         raise GqaError(name, st)
 
 
+def _current(t):
+    """The current device for a whole call in C; -1 (no device's) where t is not on one."""
+    return torch.cuda.current_device() if isinstance(t, torch.Tensor) and t.is_cuda else -1
+
+
+def _stream_handle(stream, t):
+    """The handle for a whole call in C: None for the current stream, or, for a stream of
+    another device than tensor t's, what sends the call to the checks in Python."""
+    if stream is None:
+        return None
+    same = isinstance(t, torch.Tensor) and stream.device == t.device
+    return stream.cuda_stream if same else "another device"
+
+
 def _need_tensor(t, name):
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
@@ -324,6 +345,17 @@ def _rope_inputs(q_gain, k_gain, pos, axes):
 @functools.lru_cache(maxsize=64)
 def _plain_params(qk_norm, eps, rope_base):
     return RopeParams(1 if qk_norm else 0, float(eps), float(rope_base))
+
+
+@functools.lru_cache(maxsize=64)
+def _plain_params_bytes(qk_norm, eps, rope_base):
+    return bytes(_plain_params(qk_norm, eps, rope_base))
+
+
+def _params_bytes(qk_norm, eps, rope_base, scaling):
+    if scaling is None:
+        return _plain_params_bytes(qk_norm, eps, rope_base)
+    return bytes(_params(qk_norm, eps, rope_base, scaling))
 
 
 def _params(qk_norm, eps, rope_base, scaling=None):
@@ -610,9 +642,25 @@ def gqa_decode_noalloc(q, k_cache, v_cache, lens, max_len, out=None, scale=0.0, 
     return out
 
 
-def _norm_rope_append(name, q, k, v, cache_spec, cache_shape, pos0, n_tok, max_pos0, new_len,
+def _norm_rope_append(name, q, k, v, cache, cache_names, pos0, n_tok, max_pos0, new_len,
                       q_out, q_gain, k_gain, pos, axes, qk_norm, eps, rope_base, scaling, status,
                       stream):
+    """cache: the four tensors of a Q4Cache, or K's and V's and two Nones."""
+    if _fast is None:
+        load()
+    if q is not None and q_out is None:
+        _need_tensor(q, "q")
+        q_out = _new(stream, lambda: torch.empty_like(q))
+    st = _fast.append(
+        cache[2] is not None, _current(k), q, k, v, q_out, *cache, pos0, n_tok,
+        new_len, status, q_gain, k_gain, pos, max_pos0,
+        _params_bytes(qk_norm, eps, rope_base, scaling), None if axes is None else axes._inputs,
+        0 if axes is None else len(axes.pairs), _stream_handle(stream, k))
+    if st is not None:
+        if st != GQA_OK:
+            raise GqaError(name, st)
+        return q_out
+    cache_spec, cache_shape = cache_names()
     _need_tensor(k, "k")
     ks = k.shape
     if len(ks) == 4:
@@ -631,8 +679,6 @@ def _norm_rope_append(name, q, k, v, cache_spec, cache_shape, pos0, n_tok, max_p
             raise ValueError("q and k must have the same number of dims")
         Hq = q.shape[-2]
         qs = (B, T, Hq, D) if len(ks) == 4 else (B, Hq, D)
-        if q_out is None:
-            q_out = _new(stream, lambda: torch.empty_like(q))
     elif q_out is not None:
         raise ValueError("q_out without q")
     bf, i32, each = torch.bfloat16, torch.int32, (B,)
@@ -656,13 +702,16 @@ def gqa_norm_rope_append(q, k, v, k_cache, v_cache, pos0=None, n_tok=None, max_p
     axes a RopeAxes; default pos0[b] + t) and the append of k, v, in one launch.  q, k, v
     [B, T, H, D] or [B, H, D]; q may be None.  Tokens t >= n_tok[b] are left out.
     Returns q_out (a new tensor unless given; it may be q)."""
-    _need_tensor(k_cache, "k_cache")
-    cs = k_cache.shape
-    if len(cs) != 4:
-        raise ValueError("k_cache must be [B, Hkv, Lmax, D], got %s" % (tuple(cs),))
-    return _norm_rope_append("gqa_norm_rope_append", q, k, v,
-                             ("k_cache", k_cache, torch.bfloat16, cs,
-                              "v_cache", v_cache, torch.bfloat16, cs), cs,
+    def spec():
+        _need_tensor(k_cache, "k_cache")
+        cs = k_cache.shape
+        if len(cs) != 4:
+            raise ValueError("k_cache must be [B, Hkv, Lmax, D], got %s" % (tuple(cs),))
+        if v_cache is None:
+            raise TypeError("v_cache must be a torch.Tensor")
+        return ("k_cache", k_cache, torch.bfloat16, cs, "v_cache", v_cache, torch.bfloat16, cs), cs
+
+    return _norm_rope_append("gqa_norm_rope_append", q, k, v, (k_cache, v_cache, None, None), spec,
                              pos0, n_tok, max_pos0, new_len, q_out, q_gain, k_gain, pos, axes,
                              qk_norm, eps, rope_base, scaling, status, stream)
 
@@ -673,9 +722,10 @@ def gqa_norm_rope_append_q4(q, k, v, cache, pos0=None, n_tok=None, max_pos0=-1, 
                             stream=None):
     """gqa_norm_rope_append into a 4-bit cache (a Q4Cache)."""
     _need_q4(cache)
-    return _norm_rope_append("gqa_norm_rope_append_q4", q, k, v, cache._spec(), cache.shape, pos0,
-                             n_tok, max_pos0, new_len, q_out, q_gain, k_gain, pos, axes, qk_norm,
-                             eps, rope_base, scaling, status, stream)
+    return _norm_rope_append("gqa_norm_rope_append_q4", q, k, v, cache._parts(),
+                             lambda: (cache._spec(), cache.shape), pos0, n_tok, max_pos0, new_len,
+                             q_out, q_gain, k_gain, pos, axes, qk_norm, eps, rope_base, scaling,
+                             status, stream)
 
 
 def _need_q4(cache):
@@ -702,26 +752,44 @@ def gqa_norm_rope_append_backward(q, k, dq_out, dk_cache, dv_cache, pos0=None, m
     dq_out [B, T, Hq, D] and dk_cache, dv_cache [B, Hkv, Lmax, D] those of its outputs
     (slots pos0[b] .. pos0[b] + T - 1 are read).  dq_gain, dk_gain are float32 [D], or
     None without qk_norm."""
+    name = "gqa_norm_rope_append_backward"
+    _need_tensor(q, "q")
+    _need_tensor(k, "k")
+    dev = q.device
+    if _fast is None:
+        load()
+    dq = _new(stream, lambda: torch.empty_like(q)) if dq is None else dq
+    dk = _new(stream, lambda: torch.empty_like(k)) if dk is None else dk
+    dv = _new(stream, lambda: torch.empty_like(k)) if dv is None else dv
+    both = None
+    if qk_norm and dev.type == "cuda":
+        both = _new(stream, lambda: torch.empty(2, q.shape[-1], dtype=torch.float32, device=dev))
+        if workspace is None:
+            workspace = _new(stream, lambda: norm_rope_backward_workspace(q.shape[-1], dev))
+    dg = (None, None) if both is None else both.unbind(0)
+    st = _fast.backward(
+        _current(q), q, k, dq_out, dk_cache, dv_cache, dq, dk, dv, both, pos0, workspace, status,
+        q_gain, k_gain, pos, max_pos0,
+        _params_bytes(qk_norm, eps, rope_base, scaling), None if axes is None else axes._inputs,
+        0 if axes is None else len(axes.pairs), _stream_handle(stream, q))
+    if st is not None:
+        if st != GQA_OK:
+            raise GqaError(name, st)
+        return dq, dk, dv, dg[0], dg[1]
     for name, t in (("q", q), ("k", k), ("dk_cache", dk_cache)):
         _need_tensor(t, name)
         if t.dim() != 4:
             raise ValueError("%s must have 4 dims, got %s" % (name, tuple(t.shape)))
     qs = q.shape
     B, T, Hq, D = qs
-    Hkv, Lmax, dev = k.shape[2], dk_cache.shape[2], q.device
+    Hkv, Lmax = k.shape[2], dk_cache.shape[2]
     ks, cs = (B, T, Hkv, D), (B, Hkv, Lmax, D)
     if dq_out is None or dv_cache is None:
         raise TypeError("dq_out and dv_cache must be tensors")
-    dq = _new(stream, lambda: torch.empty_like(q)) if dq is None else dq
-    dk = _new(stream, lambda: torch.empty_like(k)) if dk is None else dk
-    dv = _new(stream, lambda: torch.empty_like(k)) if dv is None else dv
     bf = torch.bfloat16
     rope = _rope_spec(B, T, D, q_gain, k_gain, pos, axes, qk_norm)
-    dg, ws_bytes = (None, None), 0
-    if qk_norm and dev.type == "cuda":
-        dg = _new(stream, lambda: torch.empty(2, D, dtype=torch.float32, device=dev)).unbind(0)
-        if workspace is None:
-            workspace = _new(stream, lambda: norm_rope_backward_workspace(D, dev))
+    ws_bytes = 0
+    if workspace is not None:
         _need_tensor(workspace, "workspace")
         ws_bytes = workspace.numel()
     p = _pointers(dev, ("q", q, bf, qs, "k", k, bf, ks, "dq_out", dq_out, bf, qs,
@@ -751,6 +819,13 @@ def kv_cache_read_q4(cache, k_out=None, v_out=None, first=None, count=None, stat
     if k_out is None:
         k_out, v_out = (_new(stream, lambda: torch.zeros(B, Hkv, Lmax, D, dtype=torch.bfloat16,
                                                          device=dev)) for _ in range(2))
+    st = _fast.read_back(_current(k_out), cache.k_codes, cache.k_scales, cache.v_codes,
+                    cache.v_scales, first, count, k_out, v_out, status,
+                    _stream_handle(stream, k_out))
+    if st is not None:
+        if st != GQA_OK:
+            raise GqaError("kv_cache_read_q4", st)
+        return k_out, v_out
     _need_tensor(k_out, "k_out")
     if k_out.dim() != 4:
         raise ValueError("k_out must be [B, Hkv, Lout, D], got %s" % (tuple(k_out.shape),))
@@ -791,6 +866,13 @@ def gqa_decode_q4(q, cache, lens, max_len, out=None, workspace=None, scale=0.0, 
         out = _new(stream, lambda: torch.empty_like(q))
     if workspace is None:
         workspace = _new(stream, lambda: decode_q4_workspace(B, Hq, Hkv, D, max_len, dev))
+    st = _fast.decode(_current(q), cache.k_codes, cache.k_scales, cache.v_codes,
+                      cache.v_scales, q, lens, max_len, out, float(scale), workspace, status,
+                      _stream_handle(stream, q))
+    if st is not None:
+        if st != GQA_OK:
+            raise GqaError("gqa_decode_q4", st)
+        return out
     _need_tensor(workspace, "workspace")
     bf = torch.bfloat16
     p = _pointers(dev, ("q", q, bf, shape) + cache._spec() +

@@ -59,12 +59,12 @@ def _compile(src: str, verbose: bool) -> tuple[str, str]:
 
 def _build_args(force: bool) -> None:
     if not force and os.path.exists(ARGS_LIB) and \
-            os.path.getmtime(ARGS_LIB) >= os.path.getmtime(ARGS_SRC):
+            os.path.getmtime(ARGS_LIB) >= max(os.path.getmtime(f) for f in [ARGS_SRC] + _headers()):
         return
     import torch
     tmp = ARGS_LIB + ".tmp%d" % os.getpid()
     cmd = [shutil.which("gcc") or "gcc", "-O2", "-Wall", "-shared", "-fPIC",
-           "-I", sysconfig.get_paths()["include"],
+           "-I", sysconfig.get_paths()["include"], "-I", os.path.join(ROOT, "include"),
            "-I", os.path.join(os.path.dirname(torch.__file__), "include"), ARGS_SRC, "-o", tmp]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:

@@ -475,3 +475,43 @@ def test_decode_graph_with_learned_gains_on_the_bf16_cache(cuda_lib):
         assert torch.equal(got, gqa.gqa_decode(qr, *b, cur, L))
     assert dg.status.item() == 0
     assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_the_checks_in_python_lead_to_the_same_calls(cuda_lib, monkeypatch):
+    """What the native argument checks do not take goes through the checks in Python:
+    the same results, and a stream of the caller's, either way."""
+    from types import SimpleNamespace
+
+    from rope_gqa_kv_b200 import _lib
+    g = torch.Generator().manual_seed(50)
+    new = lambda *s: torch.randn(*s, generator=g).to(BF).to(DEV)
+    q, k, v = new(2, 5, 4, 64), new(2, 5, 2, 64), new(2, 5, 2, 64)
+    gain, ax = new(64), gqa.RopeAxes((10, 22))
+    pos = torch.randint(0, 50, (2, 2, 5), generator=g).to(torch.int32).to(DEV)
+    pos0 = torch.tensor([0, 9], dtype=torch.int32, device=DEV)
+    kw = dict(pos0=pos0, q_gain=gain, k_gain=gain, pos=pos, axes=ax)
+
+    def run(stream=None):
+        cache = gqa.Q4Cache.zeros(2, 2, 128, 64)
+        kc, vc = (torch.zeros(2, 2, 128, 64, dtype=BF, device=DEV) for _ in range(2))
+        lens = torch.zeros(2, dtype=torch.int32, device=DEV)
+        torch.cuda.synchronize()
+        a = gqa.gqa_norm_rope_append(q, k, v, kc, vc, stream=stream, **kw)
+        b = gqa.gqa_norm_rope_append_q4(q, k, v, cache, new_len=lens, stream=stream, **kw)
+        ko, vo = gqa.kv_cache_read_q4(cache, count=lens, stream=stream)
+        out = gqa.gqa_decode_q4(q[:, 4].contiguous(), cache, lens, 20, stream=stream)
+        grads = gqa.gqa_norm_rope_append_backward(q, k, q, kc, vc, stream=stream, **kw)
+        torch.cuda.synchronize()
+        return (a, b, kc, vc, ko, vo, out) + grads + _parts(cache)
+
+    want = run()
+    side = torch.cuda.Stream()
+    fast = run(side)
+    none = lambda *a: None
+    monkeypatch.setattr(_lib, "_fast", SimpleNamespace(
+        append=none, backward=none, read_back=none, decode=none, cache=none))
+    slow = run()
+    monkeypatch.setattr(_lib, "_fast_pointers", none)
+    slower = run(side)
+    for got in (fast, slow, slower):
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
