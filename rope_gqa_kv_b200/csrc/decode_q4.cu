@@ -186,16 +186,18 @@ decode_q4_kernel(const DecQ4Args A) {
     // the newest slot) before reading; the merge may then be scheduled.
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
-    const int c = blockIdx.x;
-    const int kvh = blockIdx.y / A.n_sub, sub = blockIdx.y - kvh * A.n_sub;
-    const int b = blockIdx.z;
+    // Chunks in the slowest order: those behind the shorter sequences' ends, which have
+    // nothing to do, come last.
+    const int c = blockIdx.z;
+    const int kvh = blockIdx.x / A.n_sub, sub = blockIdx.x - kvh * A.n_sub;
+    const int b = blockIdx.y;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int group = A.Hq / A.Hkv;
     const int h0 = kvh * group + sub * A.G;                // first query head
     const int G = min(A.G, group - sub * A.G);             // query heads of this CTA
     const int len = A.lens[b];
     if (len < 1 || len > A.max_len || len > A.Lmax) {
-        if (c == 0 && blockIdx.y == 0 && tid == 0)
+        if (c == 0 && blockIdx.x == 0 && tid == 0)
             report(A.status, len < 1 ? GQA_DEV_BAD_LEN : GQA_DEV_CAPACITY);
         if (A.n_splits == 1)
             for (int i = tid; i < G * D; i += kThreads) A.out[((size_t)b * A.Hq + h0) * D + i] = 0;
@@ -561,10 +563,10 @@ decode_q4_kernel(const DecQ4Args A) {
 }
 
 // Merges the chunks of each (sequence, query head) row.  WPR warps share a row and
-// take groups of 32 of its chunks in turn, lane i owning coordinates 4 i .. 4 i + 3:
+// take groups of N of its chunks in turn, lane i owning coordinates 4 i .. 4 i + 3:
 // all partials of a group are loaded before any is used, lane i holds chunk i's
 // (m, l), and the weights travel by shuffle.
-template <int D, int WPR>
+template <int D, int WPR, int N>
 __global__ void __launch_bounds__(128)
 decode_q4_merge_kernel(const float *__restrict__ ws_ml, const float *__restrict__ ws_o,
                        const int32_t *__restrict__ lens, int max_len, int Hq, int Lmax, int chunk,
@@ -590,11 +592,11 @@ decode_q4_merge_kernel(const float *__restrict__ ws_ml, const float *__restrict_
     const float *po = ws_o + (size_t)row * n_splits * D + lane * 4;
     float M = -INFINITY, L = 0.f;
     float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
-    for (int base = 32 * part; base < ns; base += 32 * WPR) {
-        const int n = min(32, ns - base);
-        float4 pv[32];
+    for (int base = N * part; base < ns; base += N * WPR) {
+        const int n = min(N, ns - base);
+        float4 pv[N];
 #pragma unroll
-        for (int jj = 0; jj < 32; ++jj)
+        for (int jj = 0; jj < N; ++jj)
             pv[jj] = (live && jj < n)
                          ? *reinterpret_cast<const float4 *>(po + (size_t)(base + jj) * D)
                          : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -610,7 +612,7 @@ decode_q4_merge_kernel(const float *__restrict__ ws_ml, const float *__restrict_
         a3 *= alpha;
         M = mn;
 #pragma unroll
-        for (int jj = 0; jj < 32; ++jj) {
+        for (int jj = 0; jj < N; ++jj) {
             const float wj = __shfl_sync(0xffffffffu, w, jj);
             a0 = fmaf(wj, pv[jj].x, a0);
             a1 = fmaf(wj, pv[jj].y, a1);
@@ -656,8 +658,8 @@ struct Plan {
 };
 
 constexpr int kSlots = 148 * 4;        // CTAs resident at once
-constexpr int kLongChunk = 256;        // slots from which a warp takes two tiles at a time
-constexpr int kWaves = 3;              // and how many of each a full-length call should have
+constexpr int kLongChunk = 128;        // slots from which a warp takes two tiles at a time
+constexpr int kWaves = 2;              // and how many of each a full-length call should have
 
 Plan make_plan(int B, int Hq, int Hkv, int max_len) {
     Plan P;
@@ -684,7 +686,7 @@ cudaError_t launch_split(const DecQ4Args &A, cudaStream_t s) {
     pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     pdl[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(A.n_splits, A.Hkv * A.n_sub, A.B);
+    cfg.gridDim = dim3(A.Hkv * A.n_sub, A.B, A.n_splits);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = S::kSmem;
     cfg.stream = s;
@@ -714,14 +716,16 @@ cudaError_t launch_decode(const DecQ4Args &A, cudaStream_t s) {
     const cudaError_t e = A.chunk >= kLongChunk ? launch_split<D, 2>(A, s)
                                                 : launch_split<D, 1>(A, s);
     if (e != cudaSuccess || A.n_splits == 1) return e;
+    // One warp a row while a group covers its chunks, four beyond 32.
     const int rows = A.B * A.Hq;
-    if (A.n_splits > 32)               // one group of 32 chunks is one warp's work
-        return launch_pdl(decode_q4_merge_kernel<D, 4>, (unsigned)rows, 128, s,
-                          (const float *)A.ws_ml, (const float *)A.ws_o, A.lens, A.max_len, A.Hq,
-                          A.Lmax, A.chunk, A.n_splits, rows, A.out);
-    return launch_pdl(decode_q4_merge_kernel<D, 1>, (unsigned)((rows + 3) / 4), 128, s,
-                      (const float *)A.ws_ml, (const float *)A.ws_o, A.lens, A.max_len, A.Hq,
-                      A.Lmax, A.chunk, A.n_splits, rows, A.out);
+    auto merge = [&](auto kern, int grid) {
+        return launch_pdl(kern, dim3((unsigned)grid), 128, s, (const float *)A.ws_ml,
+                          (const float *)A.ws_o, A.lens, A.max_len, A.Hq, A.Lmax, A.chunk,
+                          A.n_splits, rows, A.out);
+    };
+    if (A.n_splits > 32) return merge(decode_q4_merge_kernel<D, 4, 32>, rows);
+    if (A.n_splits > 8) return merge(decode_q4_merge_kernel<D, 1, 32>, (rows + 3) / 4);
+    return merge(decode_q4_merge_kernel<D, 1, 8>, (rows + 3) / 4);
 }
 
 // ---------------------------------------------------------------------------
