@@ -25,7 +25,7 @@ namespace {
 
 constexpr int kWarps = 4;              // warps per CTA
 constexpr int kResident = 5;           // CTAs per SM
-constexpr int kRing = 8;               // passes on their way or waiting, per warp
+constexpr int kRing = 3;               // passes on their way or waiting, per warp
 
 struct AxisTable {
     uint8_t axis[64];
@@ -46,16 +46,34 @@ struct AppendArgs {
     float eps;
 };
 
+// The token's positions on the axes of the pairs that the lane works out: pairs lane and
+// lane + 32.
+template <int D>
+struct Positions {
+    static constexpr int N = (D / 2 + 31) / 32;
+    int p[N];
+
+    __device__ __forceinline__ void load(const int32_t *pos, int p_seq, int B, int T, int b, int t,
+                                         const AxisTable &ax, int lane) {
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            const int i = lane + 32 * n;
+            p[n] = p_seq;
+            if (pos && i < D / 2) p[n] = pos[((size_t)ax.axis[i] * B + b) * T + t];
+        }
+    }
+};
+
 // cos / sin of the token's D/2 angles into the warp's rows: position times theta_i
 // in float64, reduced to [-pi, pi] in float64, then fp32.
 template <int D>
-__device__ __forceinline__ void token_angles(float *cs, float *sn, const int32_t *pos, int p_seq,
-                                             int B, int T, int b, int t, const RopeTable &tab,
-                                             const AxisTable &ax, int lane) {
+__device__ __forceinline__ void token_angles(float *cs, float *sn, const Positions<D> &pos,
+                                             const RopeTable &tab, int lane) {
 #pragma unroll
-    for (int i = lane; i < D / 2; i += 32) {
-        const int p = pos ? pos[((size_t)ax.axis[i] * B + b) * T + t] : p_seq;
-        const double a = (double)p * tab.theta[i];
+    for (int n = 0; n < Positions<D>::N; ++n) {
+        const int i = lane + 32 * n;
+        if (i >= D / 2) break;
+        const double a = (double)pos.p[n] * tab.theta[i];
         const double two_pi = 6.283185307179586476925286766559;
         const double r = a - rint(a * (1.0 / two_pi)) * two_pi;
         float sf, cf;
@@ -264,10 +282,13 @@ norm_rope_append_kernel(const AppendArgs A, const __grid_constant__ RopeTable ta
     __syncthreads();                                       // only warp-level sync follows
 
     int stage = 0;
+#pragma unroll 1
     for (; at.find(A); at.unit += at.stride) {
+        const int tok = at.tok, b = at.b, slot_row = at.slot_row, slice = at.slice;
+        Positions<D> pos;
+        pos.load(A.pos, slot_row, A.B, A.T, b, at.t, ax, lane);
         __syncwarp();                                      // the last unit's angles are read
-        token_angles<D>(cs[warp], sn[warp], A.pos, at.slot_row, A.B, A.T, at.b, at.t, tab, ax,
-                        lane);
+        token_angles<D>(cs[warp], sn[warp], pos, tab, lane);
         __syncwarp();
         Turn turn;
         int end = 0, left = 0;                             // as of the loads
@@ -275,15 +296,15 @@ norm_rope_append_kernel(const AppendArgs A, const __grid_constant__ RopeTable ta
         uint16_t *dst = nullptr;                           // the lane's first chunk (not Q4's K, V)
         size_t row = 0;                                    // the cache row
 #pragma unroll 1
-        for (int ps = at.slice; ps < npass; ps += A.n_slices) {
+        for (int ps = slice; ps < npass; ps += A.n_slices) {
             if (ps >= end) {                               // the first pass of a kind: uniform
                 is_q = ps < qp;
                 is_k = !is_q && ps < qp + kp;
                 end = is_q ? qp : is_k ? qp + kp : npass;
                 const int h = (ps - (is_q ? 0 : is_k ? qp : qp + kp)) * S::kVecPerWarp + slot;
                 left = active ? (is_q ? A.Hq : A.Hkv) - h : 0;
-                row = ((size_t)at.b * A.Hkv + h) * A.Lmax + at.slot_row;
-                if (is_q) dst = A.q_out + ((size_t)at.tok * A.Hq + h) * D + 8 * j;
+                row = ((size_t)b * A.Hkv + h) * A.Lmax + slot_row;
+                if (is_q) dst = A.q_out + ((size_t)tok * A.Hq + h) * D + 8 * j;
                 else if (!Q4) dst = (is_k ? A.kc : A.vc) + row * D + 8 * j;
                 if (is_q || is_k) make_turn<D>(turn, cs[warp], sn[warp], gain[is_k], j, active);
             }
@@ -341,7 +362,7 @@ norm_rope_append_kernel(const AppendArgs A, const __grid_constant__ RopeTable ta
 constexpr int kBwdWarps = 4;
 constexpr int kBwdResident = 3;                            // CTAs per SM
 constexpr int kBwdMaxCtas = 148 * kBwdResident;
-constexpr int kBwdRing = 5;                                // passes on their way or waiting
+constexpr int kBwdRing = 4;                                // passes on their way or waiting
 
 struct BackwardArgs {
     const uint16_t *q, *k, *dq_out, *dkc, *dvc;
@@ -502,15 +523,23 @@ __device__ __forceinline__ void backward_units(const BackwardArgs &A, const Rope
     for (int i = 0; i < kBwdRing - 1; ++i) load_next(i);
 
     int stage = 0;
-    unsigned at_tok = 0, at_b = 0;
-    int at_row = 0, ps = 0;
+    unsigned next_tok = 0, next_b = 0;
+    int next_row = 0, next_ps = 0;
+    Positions<D> pos;                  // of the warp's next token, as in the forward
+    unsigned u = find(cta * kBwdWarps + warp, next_tok, next_b, next_row, next_ps);
+    if (u < units)
+        pos.load(A.pos, next_row, A.B, A.T, (int)next_b, (int)(next_tok - next_b * A.T), ax, lane);
 #pragma unroll 1
-    for (unsigned u = cta * kBwdWarps + warp;
-         (u = find(u, at_tok, at_b, at_row, ps)) < units; u += stride) {
+    while (u < units) {
         __syncwarp();                                      // the warp's last unit has read its angles
-        token_angles<D>(sh.cs[warp], sh.sn[warp], A.pos, at_row, A.B, A.T, (int)at_b,
-                        (int)(at_tok - at_b * A.T), tab, ax, lane);
+        token_angles<D>(sh.cs[warp], sh.sn[warp], pos, tab, lane);
         __syncwarp();
+        const unsigned at_tok = next_tok;
+        int ps = next_ps;
+        u = find(u + stride, next_tok, next_b, next_row, next_ps);
+        if (u < units)
+            pos.load(A.pos, next_row, A.B, A.T, (int)next_b, (int)(next_tok - next_b * A.T), ax,
+                     lane);
         float c[8], s[8];
         lane_angles<D>(sh.cs[warp], sh.sn[warp], j, active, c, s);
         int end = 0, left = 0;
