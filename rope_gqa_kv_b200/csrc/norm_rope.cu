@@ -40,8 +40,7 @@ struct AppendArgs {
     const uint16_t *q_gain, *k_gain;
     const int32_t *pos0, *n_tok, *pos;
     int32_t *new_len, *status;
-    int B, T, Hq, Hkv, Lmax, n_slices;
-    unsigned units;                    // tokens x slices
+    int B, T, Hq, Hkv, Lmax, n_slices; // slices of a token's passes
     int qk_norm;
     float eps;
 };
@@ -177,27 +176,47 @@ __device__ __forceinline__ void copy_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// A warp's way through its units: unit, unit + stride, .. below units, those whose
-// token is not to be written left out.
+// A warp's way through its units -- unit, unit + stride, .. -- a unit being a slice of a
+// token's passes: the slice, its token t of sequence b.  The steps are taken without a
+// division.
 struct Walk {
-    unsigned unit, stride, units;
-    int tok, b, t, slice, slot_row;
+    int b, t, slice;
+    int step_b, step_t, step_slice;
 
-    // To the first live unit from `unit` on; false behind the last.
-    __device__ __forceinline__ bool find(const AppendArgs &A) {
-        for (; unit < units; unit += stride) {
-            tok = (int)(unit / (unsigned)A.n_slices);
-            slice = (int)(unit - (unsigned)tok * A.n_slices);
-            b = tok / A.T;
-            t = tok - b * A.T;
-            const int p0 = A.pos0 ? A.pos0[b] : 0;
-            const int n = A.n_tok ? A.n_tok[b] : A.T;
-            slot_row = p0 + t;
-            if (p0 >= 0 && n >= 0 && n <= A.T && (long long)p0 + n <= A.Lmax && t < n) return true;
+    __device__ __forceinline__ void start(unsigned unit, unsigned stride, int n_slices, int T) {
+        const unsigned tok = unit / (unsigned)n_slices, step = stride / (unsigned)n_slices;
+        slice = (int)(unit - tok * n_slices);
+        step_slice = (int)(stride - step * n_slices);
+        b = (int)(tok / (unsigned)T);
+        step_b = (int)(step / (unsigned)T);
+        t = (int)(tok - (unsigned)b * T);
+        step_t = (int)(step - (unsigned)step_b * T);
+    }
+    __device__ __forceinline__ void step(int n_slices, int T) {
+        b += step_b;
+        t += step_t;
+        slice += step_slice;
+        if (slice >= n_slices) {
+            slice -= n_slices;
+            ++t;
         }
-        return false;
+        if (t >= T) {
+            t -= T;
+            ++b;
+        }
     }
 };
+
+// On to the first unit whose token is to be written; false behind the last.
+__device__ __forceinline__ bool find_live(Walk &w, const AppendArgs &A, int &slot_row) {
+    for (; w.b < A.B; w.step(A.n_slices, A.T)) {
+        const int p0 = A.pos0 ? A.pos0[w.b] : 0;
+        const int n = A.n_tok ? A.n_tok[w.b] : A.T;
+        slot_row = p0 + w.t;
+        if (p0 >= 0 && n >= 0 && n <= A.T && (long long)p0 + n <= A.Lmax && w.t < n) return true;
+    }
+    return false;
+}
 
 template <int D, bool Q4>
 __global__ void __launch_bounds__(kWarps * 32, kResident)
@@ -225,13 +244,12 @@ norm_rope_append_kernel(const AppendArgs A, const __grid_constant__ RopeTable ta
     const int npass = qp + 2 * kp;
 
     Walk ahead;                        // of the loads
-    ahead.unit = blockIdx.x * kWarps + warp;
-    ahead.stride = gridDim.x * kWarps;
-    ahead.units = A.units;
+    ahead.start(blockIdx.x * kWarps + warp, gridDim.x * kWarps, A.n_slices, A.T);
     Walk at = ahead;                   // of the arithmetic
     const uint32_t mine = static_cast<uint32_t>(__cvta_generic_to_shared(&ring[warp][0][0][lane]));
     const int step_h = A.n_slices * S::kVecPerWarp;        // heads from pass to pass
-    bool more = ahead.find(A);
+    int row_ahead = 0;
+    bool more = find_live(ahead, A, row_ahead);
     int ps_ahead = ahead.slice, end_ahead = 0;             // next pass, end of its kind
     int left_ahead = 0;                                    // heads of its kind from the lane's on
     const uint16_t *src = nullptr;
@@ -243,7 +261,7 @@ norm_rope_append_kernel(const AppendArgs A, const __grid_constant__ RopeTable ta
                 end_ahead = is_q ? qp : is_k ? qp + kp : npass;
                 const int h = (ps_ahead - (is_q ? 0 : is_k ? qp : qp + kp)) * S::kVecPerWarp + slot;
                 const int heads = is_q ? A.Hq : A.Hkv;
-                src = (is_q ? A.q : is_k ? A.k : A.v) + ((size_t)ahead.tok * heads + h) * D + 8 * j;
+                src = (is_q ? A.q : is_k ? A.k : A.v) + (((size_t)ahead.b * A.T + ahead.t) * heads + h) * D + 8 * j;
                 left_ahead = active ? heads - h : 0;
             }
             if (left_ahead > 0) {
@@ -254,22 +272,19 @@ norm_rope_append_kernel(const AppendArgs A, const __grid_constant__ RopeTable ta
             left_ahead -= step_h;
             ps_ahead += A.n_slices;
             if (ps_ahead >= npass) {
-                ahead.unit += ahead.stride;
-                more = ahead.find(A);
+                ahead.step(A.n_slices, A.T);
+                more = find_live(ahead, A, row_ahead);
                 ps_ahead = ahead.slice;
                 end_ahead = 0;
             }
         }
         copy_commit();
     };
-#pragma unroll
+#pragma unroll 1
     for (int i = 0; i < kRing - 1; ++i) load_next(i);
 
-    // Lengths and errors of the sequences, by the units of their first tokens.
-    for (unsigned u = blockIdx.x * kWarps + warp; u < A.units; u += gridDim.x * kWarps) {
-        const unsigned tok = u / (unsigned)A.n_slices;
-        if (tok * A.n_slices != u || tok % (unsigned)A.T != 0 || lane != 0) continue;
-        const int b = (int)(tok / (unsigned)A.T);
+    // Lengths and errors of the sequences.
+    for (int b = blockIdx.x * kWarps * 32 + threadIdx.x; b < A.B; b += gridDim.x * kWarps * 32) {
         const int p0 = A.pos0 ? A.pos0[b] : 0;
         const int n = A.n_tok ? A.n_tok[b] : A.T;
         const bool bad = p0 < 0 || n < 0 || n > A.T;
@@ -283,8 +298,9 @@ norm_rope_append_kernel(const AppendArgs A, const __grid_constant__ RopeTable ta
 
     int stage = 0;
 #pragma unroll 1
-    for (; at.find(A); at.unit += at.stride) {
-        const int tok = at.tok, b = at.b, slot_row = at.slot_row, slice = at.slice;
+    for (int slot_row = 0; find_live(at, A, slot_row); at.step(A.n_slices, A.T)) {
+        const int b = at.b;
+        const size_t tok = (size_t)b * A.T + at.t;
         Positions<D> pos;
         pos.load(A.pos, slot_row, A.B, A.T, b, at.t, ax, lane);
         __syncwarp();                                      // the last unit's angles are read
@@ -296,7 +312,7 @@ norm_rope_append_kernel(const AppendArgs A, const __grid_constant__ RopeTable ta
         uint16_t *dst = nullptr;                           // the lane's first chunk (not Q4's K, V)
         size_t row = 0;                                    // the cache row
 #pragma unroll 1
-        for (int ps = slice; ps < npass; ps += A.n_slices) {
+        for (int ps = at.slice; ps < npass; ps += A.n_slices) {
             if (ps >= end) {                               // the first pass of a kind: uniform
                 is_q = ps < qp;
                 is_k = !is_q && ps < qp + kp;
@@ -304,7 +320,7 @@ norm_rope_append_kernel(const AppendArgs A, const __grid_constant__ RopeTable ta
                 const int h = (ps - (is_q ? 0 : is_k ? qp : qp + kp)) * S::kVecPerWarp + slot;
                 left = active ? (is_q ? A.Hq : A.Hkv) - h : 0;
                 row = ((size_t)b * A.Hkv + h) * A.Lmax + slot_row;
-                if (is_q) dst = A.q_out + ((size_t)tok * A.Hq + h) * D + 8 * j;
+                if (is_q) dst = A.q_out + (tok * A.Hq + h) * D + 8 * j;
                 else if (!Q4) dst = (is_k ? A.kc : A.vc) + row * D + 8 * j;
                 if (is_q || is_k) make_turn<D>(turn, cs[warp], sn[warp], gain[is_k], j, active);
             }
@@ -374,7 +390,6 @@ struct BackwardArgs {
     int B, T, Hq, Hkv, Lmax;
     int n_q;                           // CTAs of the query passes; the rest: keys and values
     int slices[2];                     // slices of a token's passes: query, key and value
-    unsigned units[2];                 // tokens x slices
     int qk_norm;
     float eps;
 };
@@ -449,7 +464,7 @@ __device__ __forceinline__ void backward_units(const BackwardArgs &A, const Rope
     const int heads = QUERIES ? A.Hq : A.Hkv;
     const int per_kind = (heads + S::kVecPerWarp - 1) / S::kVecPerWarp;
     const int npass = QUERIES ? per_kind : 2 * per_kind;
-    const unsigned n_slices = A.slices[QUERIES ? 0 : 1], units = A.units[QUERIES ? 0 : 1];
+    const int n_slices = A.slices[QUERIES ? 0 : 1];
     const int cta = QUERIES ? (int)blockIdx.x : (int)blockIdx.x - A.n_q;
     const unsigned stride = (QUERIES ? A.n_q : gridDim.x - A.n_q) * kBwdWarps;
     const bool norm = A.qk_norm != 0;
@@ -465,36 +480,36 @@ __device__ __forceinline__ void backward_units(const BackwardArgs &A, const Rope
         }
     }
 
-    // Unit u: its token, sequence, cache slot and slice; the first in range from u on.
-    auto find = [&](unsigned u, unsigned &tok, unsigned &b, int &slot_row, int &slice) {
-        for (; u < units; u += stride) {
-            tok = u / n_slices;
-            b = tok / (unsigned)A.T;
-            const int p0 = A.pos0 ? A.pos0[b] : 0;
-            slot_row = p0 + (int)(tok - b * A.T);
-            slice = (int)(u - tok * n_slices);
-            if (p0 >= 0 && (long long)p0 + A.T <= A.Lmax) break;
+    // On to the first unit in range; false behind the last.
+    auto find = [&](Walk &w, int &slot_row) {
+        for (; w.b < A.B; w.step(n_slices, A.T)) {
+            const int p0 = A.pos0 ? A.pos0[w.b] : 0;
+            slot_row = p0 + w.t;
+            if (p0 >= 0 && (long long)p0 + A.T <= A.Lmax) return true;
         }
-        return u;
+        return false;
     };
-    const int step_h = (int)n_slices * S::kVecPerWarp;     // heads from pass to pass
+    const int step_h = n_slices * S::kVecPerWarp;          // heads from pass to pass
     const size_t x_step = (size_t)step_h * D, y_step = QUERIES ? x_step : x_step * A.Lmax;
 
     // The loads, kBwdRing - 1 passes ahead of the arithmetic.
-    unsigned tok = 0, b = 0;
-    int slot_row = 0, kps = 0, kend = 0, kleft = 0;
-    unsigned ku = find(cta * kBwdWarps + warp, tok, b, slot_row, kps);
+    Walk ahead;
+    ahead.start(cta * kBwdWarps + warp, stride, n_slices, A.T);
+    Walk next = ahead;                 // of the arithmetic
+    int slot_row = 0, kend = 0, kleft = 0;
+    bool more = find(ahead, slot_row);
+    int kps = ahead.slice;
     const uint16_t *xs = nullptr, *ys = nullptr;
     const uint32_t mine =
         static_cast<uint32_t>(__cvta_generic_to_shared(&sh.ring[warp][0][0][lane]));
     auto load_next = [&](int stage) {
-        if (ku < units) {                                  // uniform across the warp
+        if (more) {                                        // uniform across the warp
             const bool value = !QUERIES && kps >= per_kind;
             if (kps >= kend) {                             // the first pass of a kind
                 kend = value ? npass : per_kind;
                 const int h = (value ? kps - per_kind : kps) * S::kVecPerWarp + slot;
-                const size_t in = ((size_t)tok * heads + h) * D + 8 * j;
-                const size_t row = (((size_t)b * A.Hkv + h) * A.Lmax + slot_row) * D + 8 * j;
+                const size_t in = (((size_t)ahead.b * A.T + ahead.t) * heads + h) * D + 8 * j;
+                const size_t row = (((size_t)ahead.b * A.Hkv + h) * A.Lmax + slot_row) * D + 8 * j;
                 xs = (QUERIES ? A.q : A.k) + in;
                 ys = QUERIES ? A.dq_out + in : (value ? A.dvc : A.dkc) + row;
                 kleft = active ? heads - h : 0;
@@ -513,33 +528,33 @@ __device__ __forceinline__ void backward_units(const BackwardArgs &A, const Rope
             kleft -= step_h;
             kps += n_slices;
             if (kps >= npass) {
-                ku = find(ku + stride, tok, b, slot_row, kps);
+                ahead.step(n_slices, A.T);
+                more = find(ahead, slot_row);
+                kps = ahead.slice;
                 kend = 0;
             }
         }
         copy_commit();
     };
-#pragma unroll
+#pragma unroll 1
     for (int i = 0; i < kBwdRing - 1; ++i) load_next(i);
 
     int stage = 0;
-    unsigned next_tok = 0, next_b = 0;
-    int next_row = 0, next_ps = 0;
-    Positions<D> pos;                  // of the warp's next token, as in the forward
-    unsigned u = find(cta * kBwdWarps + warp, next_tok, next_b, next_row, next_ps);
-    if (u < units)
-        pos.load(A.pos, next_row, A.B, A.T, (int)next_b, (int)(next_tok - next_b * A.T), ax, lane);
+    int next_row = 0;
+    Positions<D> pos;                  // of the warp's next token, loaded a token ahead: under a
+                                       // full memory system that takes as long as some passes
+    bool on = find(next, next_row);
+    if (on) pos.load(A.pos, next_row, A.B, A.T, next.b, next.t, ax, lane);
 #pragma unroll 1
-    while (u < units) {
+    while (on) {
         __syncwarp();                                      // the warp's last unit has read its angles
         token_angles<D>(sh.cs[warp], sh.sn[warp], pos, tab, lane);
         __syncwarp();
-        const unsigned at_tok = next_tok;
-        int ps = next_ps;
-        u = find(u + stride, next_tok, next_b, next_row, next_ps);
-        if (u < units)
-            pos.load(A.pos, next_row, A.B, A.T, (int)next_b, (int)(next_tok - next_b * A.T), ax,
-                     lane);
+        const size_t at_tok = (size_t)next.b * A.T + next.t;
+        int ps = next.slice;
+        next.step(n_slices, A.T);
+        on = find(next, next_row);
+        if (on) pos.load(A.pos, next_row, A.B, A.T, next.b, next.t, ax, lane);
         float c[8], s[8];
         lane_angles<D>(sh.cs[warp], sh.sn[warp], j, active, c, s);
         int end = 0, left = 0;
@@ -551,7 +566,7 @@ __device__ __forceinline__ void backward_units(const BackwardArgs &A, const Rope
                 end = value ? npass : per_kind;
                 const int h = (value ? ps - per_kind : ps) * S::kVecPerWarp + slot;
                 dst = (QUERIES ? A.dq : value ? A.dv : A.dk) +
-                      ((size_t)at_tok * heads + h) * D + 8 * j;
+                      (at_tok * heads + h) * D + 8 * j;
                 left = active ? heads - h : 0;
             }
             copy_wait<kBwdRing - 2>();
@@ -662,10 +677,9 @@ cudaError_t launch_append(AppendArgs A, const gqa_rope_params &p, const gqa_rope
                       2 * ((A.Hkv + per_pass - 1) / per_pass);
     constexpr int kCtas = 148 * kResident;
     A.n_slices = slices(tokens, npass, kCtas * kWarps);
-    A.units = (unsigned)(tokens * A.n_slices);
-    const unsigned ctas = (A.units + kWarps - 1) / kWarps;
-    return launch_pdl(norm_rope_append_kernel<D, Q4>, ctas < kCtas ? ctas : kCtas, kWarps * 32, s,
-                      A, make_table(D, p), axis_table(x));
+    const long long ctas = (tokens * A.n_slices + kWarps - 1) / kWarps;
+    return launch_pdl(norm_rope_append_kernel<D, Q4>, (unsigned)(ctas < kCtas ? ctas : kCtas),
+                      kWarps * 32, s, A, make_table(D, p), axis_table(x));
 }
 
 template <int D>
@@ -675,18 +689,36 @@ cudaError_t launch_backward(BackwardArgs A, const gqa_rope_params &p, const gqa_
     const int per_pass = RopeShape<D>::kVecPerWarp;
     const int npass[2] = {(A.Hq + per_pass - 1) / per_pass,
                           2 * ((A.Hkv + per_pass - 1) / per_pass)};
-    // CTAs by the rows moved: three per query and key head, two per value head.
-    const double share = 3.0 * A.Hq / (3.0 * A.Hq + 5.0 * A.Hkv);
-    int most[2], ctas[2];
-    most[0] = (int)(kBwdMaxCtas * share + 0.5);
-    most[0] = most[0] < 1 ? 1 : most[0] > kBwdMaxCtas - 1 ? kBwdMaxCtas - 1 : most[0];
-    most[1] = kBwdMaxCtas - most[0];
-    for (int i = 0; i < 2; ++i) {
-        A.slices[i] = slices(tokens, npass[i], most[i] * kBwdWarps);
-        A.units[i] = (unsigned)(tokens * A.slices[i]);
-        const long long need = ((long long)A.units[i] + kBwdWarps - 1) / kBwdWarps;
-        ctas[i] = (int)(need < most[i] ? need : most[i]);
+    // What a token takes in either role, in passes: its angles and the rest of its start
+    // about three, a value pass, which is only copied, half a one.
+    const double cost[2] = {3.0 + npass[0], 3.0 + 0.75 * npass[1]};
+    auto warps_for = [&](int i, int n_ctas) {              // slices, and CTAs that find work
+        A.slices[i] = slices(tokens, npass[i], n_ctas * kBwdWarps);
+        const long long need = (tokens * A.slices[i] + kBwdWarps - 1) / kBwdWarps;
+        return (int)(need < n_ctas ? need : n_ctas);
+    };
+    // CTAs in that proportion.  With few tokens a warp the last, partly filled round counts:
+    // the best of the shares around it by the longer role's rounds.
+    const int even = (int)(kBwdMaxCtas * cost[0] / (cost[0] + cost[1]) + 0.5);
+    int best = even;
+    if (tokens < 16LL * kBwdMaxCtas * kBwdWarps) {
+        double least = 1e300;
+        for (int n = even - kBwdMaxCtas / 8; n <= even + kBwdMaxCtas / 8; n += 3) {
+            if (n < 1 || n >= kBwdMaxCtas) continue;
+            double longest = 0;
+            for (int i = 0; i < 2; ++i) {
+                const long long warps = (long long)(i ? kBwdMaxCtas - n : n) * kBwdWarps;
+                const double t = cost[i] * (double)((tokens + warps - 1) / warps);
+                longest = t > longest ? t : longest;
+            }
+            if (longest < least) {
+                least = longest;
+                best = n;
+            }
+        }
     }
+    best = best < 1 ? 1 : best > kBwdMaxCtas - 1 ? kBwdMaxCtas - 1 : best;
+    const int ctas[2] = {warps_for(0, best), warps_for(1, kBwdMaxCtas - best)};
     A.n_q = ctas[0];
     const int grid = ctas[0] + ctas[1];
     cudaError_t e = launch_pdl(norm_rope_backward_kernel<D>, dim3((unsigned)grid), kBwdWarps * 32,
