@@ -22,8 +22,9 @@
 //     the (s, m) words themselves, with sum(q) in three bf16 parts (24 bits).
 //   * output: sum_k p_k (m_k + s_k c_k,d).  p_k s_k is the 8-column operand, carried
 //     by movmatrix from the score layout, in fp16 after a power of two that brings the
-//     largest s so far to 2^5 .. 2^6: one rounding, 2^-12 of the term, against bf16's
-//     2^-9 (terms below 2^-20 of the largest lose bits, 2^-31 of it at most).
+//     group's largest s so far to 2^5 .. 2^6: one rounding, 2^-12 of the term, against
+//     bf16's 2^-9 (terms below 2^-20 of the group's largest lose bits, 2^-31 of it at
+//     most).
 //     sum(p m) is added up in fp32 beside it.
 // mma.sync rather than tcgen05: its operands come from registers, where the codes
 // are unpacked; tcgen05 would need them written to shared memory as bf16, four
@@ -247,7 +248,7 @@ decode_q4_kernel(const DecQ4Args A) {
         vg += S::R * kWarps * S::RB;
         sg += S::R * kWarps * S::SB;
     };
-#pragma unroll
+#pragma unroll 1
     for (int i = 0; i < kStages - 1; ++i) {
         if (warp + kWarps * i < n_units) fetch(warp + kWarps * i, i);
         copy_commit();
@@ -324,10 +325,14 @@ decode_q4_kernel(const DecQ4Args A) {
         pm[g][0] = pm[g][1] = 0.f;
     }
     // p s goes into fp16 times up = 2^(132 - eb), eb the biased exponent of the largest V
-    // step so far: p <= 2^kSlack keeps it below 2^14, and steps may double twice before
-    // the sums have to follow (cap).  o is in units of 2^(eb - 108), with the codes' 2^-24.
+    // step of the group so far: p <= 2^kSlack keeps it below 2^15, and steps may grow
+    // fourfold before the sums have to follow (cap).  o is in units of 2^(eb - 108), with
+    // the codes' 2^-24.  Lane (r, kk) keeps group kk's eb and cap.
+    const int gk = min(kk, NG - 1);
     uint32_t eb = 0;
-    float up = 0.f, cap = 0.f;
+    float cap = 0.f, up[NG];
+#pragma unroll
+    for (int g = 0; g < NG; ++g) up[g] = 0.f;
     const uint32_t sel = (r & 1) ? 0x7632u : 0x5410u;
 
     int stage = 0;
@@ -359,8 +364,8 @@ decode_q4_kernel(const DecQ4Args A) {
             load_words<NG>(w1, kw + k1 * (S::RS / 4) + NG * kk);
             load_words<NG>(x0, ksw + k0 * NG);
             load_words<NG>(x1, ksw + k1 * NG);
-            const uint32_t mk0 = ksw[k0 * NG + min(kk, NG - 1)];
-            const uint32_t mk1 = ksw[k1 * NG + min(kk, NG - 1)];
+            const uint32_t mk0 = ksw[k0 * NG + gk];
+            const uint32_t mk1 = ksw[k1 * NG + gk];
 #pragma unroll
             for (int e = 0; e < 4; ++e) sc[j][e] = 0.f;
 #pragma unroll
@@ -381,8 +386,8 @@ decode_q4_kernel(const DecQ4Args A) {
             }
             load_words<NG>(m0[j], vsw + k0 * NG);
             load_words<NG>(m1[j], vsw + k1 * NG);
-            smax = max_bf16x2(smax, max_bf16x2(vsw[k0 * NG + min(kk, NG - 1)],
-                                               vsw[k1 * NG + min(kk, NG - 1)]));
+            smax = max_bf16x2(smax, max_bf16x2(vsw[k0 * NG + gk],
+                                               vsw[k1 * NG + gk]));
         }
         if (S::R * (u + 1) > nk) {                         // the sequence ends in this unit
 #pragma unroll
@@ -401,17 +406,14 @@ decode_q4_kernel(const DecQ4Args A) {
         }
         n0 *= A.scale_log2;
         n1 *= A.scale_log2;
-        // (the lanes of a row hold one group's step each)
         if (__any_sync(0xffffffffu, fmaxf(n0 - ref[0], n1 - ref[1]) > kSlack ||
                                         bf16lo(smax) >= cap)) {
 #pragma unroll
             for (int x = 4; x < 32; x <<= 1) {
                 n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, x));
                 n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, x));
-            }
-#pragma unroll
-            for (int x = 1; x < 32; x <<= 1)
                 smax = max_bf16x2(smax, __shfl_xor_sync(0xffffffffu, smax, x));
+            }
             n0 = fmaxf(n0, ref[0]);
             n1 = fmaxf(n1, ref[1]);
             const uint32_t neb = max(eb, min(max((smax >> 7) & 0xffu, 17u), 235u));
@@ -420,23 +422,26 @@ decode_q4_kernel(const DecQ4Args A) {
             const float f0 = ex2(ref[0] - n0), f1 = ex2(ref[1] - n1);
             l[0] *= f0;
             l[1] *= f1;
+            eb = neb;
+            cap = __uint_as_float((eb + 2u) << 23);                  // 4 times the step's power
+            const float mine = __uint_as_float((259u - eb) << 23);   // 2^(132 - eb)
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
                 pm[g][0] *= f0;
                 pm[g][1] *= f1;
+                up[g] = __shfl_sync(0xffffffffu, mine, g);
+                const float fg = __shfl_sync(0xffffffffu, es, g);
+                const float h0g = f0 * fg, h1g = f1 * fg;
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    o[g][e][0] *= f0 * es;
-                    o[g][e][1] *= f1 * es;
-                    o[g][e][2] *= f0 * es;
-                    o[g][e][3] *= f1 * es;
+                    o[g][e][0] *= h0g;
+                    o[g][e][1] *= h1g;
+                    o[g][e][2] *= h0g;
+                    o[g][e][3] *= h1g;
                 }
             }
             ref[0] = n0;
             ref[1] = n1;
-            eb = neb;
-            up = __uint_as_float((259u - eb) << 23);                 // 2^(132 - eb)
-            cap = __uint_as_float((eb + 2u) << 23);                  // 4 times the step's power
         }
 
         // ---- output: rows = coordinates, columns = heads ----
@@ -452,16 +457,14 @@ decode_q4_kernel(const DecQ4Args A) {
             load_words<NG>(wb, vr + vb * (S::RS / 4));
             load_words<NG>(wc, vr + (va + 8) * (S::RS / 4));
             load_words<NG>(wd, vr + (vb + 8) * (S::RS / 4));
-            const float p0 = sc[j][0] * up, p1 = sc[j][1] * up;
-            const float p2 = sc[j][2] * up, p3 = sc[j][3] * up;
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
-                const float s0 = bf16lo(m0[j][g]), s1 = bf16lo(m1[j][g]);
+                const float s0 = bf16lo(m0[j][g]) * up[g], s1 = bf16lo(m1[j][g]) * up[g];
                 const float z0 = bf16hi(m0[j][g]), z1 = bf16hi(m1[j][g]);
                 pm[g][0] = fmaf(z0, sc[j][0], fmaf(z1, sc[j][2], pm[g][0]));
                 pm[g][1] = fmaf(z0, sc[j][1], fmaf(z1, sc[j][3], pm[g][1]));
-                const uint32_t b0 = transpose8(pack_f16x2(p0 * s0, p1 * s0));
-                const uint32_t b1 = transpose8(pack_f16x2(p2 * s1, p3 * s1));
+                const uint32_t b0 = transpose8(pack_f16x2(sc[j][0] * s0, sc[j][1] * s0));
+                const uint32_t b1 = transpose8(pack_f16x2(sc[j][2] * s1, sc[j][3] * s1));
                 // Rows r + 8 get the whole bytes, 16 times the upper code plus the lower:
                 // one instruction fewer, and the lower ones' sums are in rows r.
                 const uint32_t y0 = __byte_perm(wa[g], wb[g], sel);
@@ -478,8 +481,7 @@ decode_q4_kernel(const DecQ4Args A) {
     copy_wait<0>();
     __syncthreads();
     float *part = reinterpret_cast<float *>(smem);         // [warp][column][D + 4]
-    const float down = __uint_as_float((eb + 19u) << 23);            // 2^(eb - 108)
-    const float down16 = down * 0.0625f;
+    const float mine = __uint_as_float((eb + 19u) << 23);            // 2^(eb - 108)
 #pragma unroll
     for (int x = 4; x < 32; x <<= 1) {
         l[0] += __shfl_xor_sync(0xffffffffu, l[0], x);
@@ -487,6 +489,7 @@ decode_q4_kernel(const DecQ4Args A) {
     }
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
+        const float down = __shfl_sync(0xffffffffu, mine, g), down16 = down * 0.0625f;
         float d0 = pm[g][0], d1 = pm[g][1];
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) {

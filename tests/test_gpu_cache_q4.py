@@ -260,6 +260,31 @@ def test_decode_constant_groups_and_nan_keys(cuda_lib):
     assert torch.isnan(out[1, 2:]).all() and torch.isfinite(out[1, :2]).all()
 
 
+def _times(scales, factor):
+    """The (s, m) pairs times powers of two (exact)."""
+    return (scales.double() * factor).to(BF)
+
+
+@pytest.mark.parametrize("D", [64, 96, 128])
+@pytest.mark.parametrize("n", [60, 700])
+def test_decode_far_apart_magnitudes(cuda_lib, D, n):
+    """Values whose steps lie 2^30 apart from group to group, grow or shrink by 2^100
+    along the sequence, or are very small or large throughout; q and K far from 1."""
+    L, lens = 768, torch.tensor([n, n - 13])
+    q = torch.randn(2, 6, D, generator=torch.Generator().manual_seed(n)).to(BF)
+    base = _random_cache(n + D, 2, 2, L, D)
+    ng = D // 32
+    groups = torch.exp2(30.0 * torch.arange(ng, dtype=torch.float64) - 45).view(1, 1, 1, ng, 1)
+    rows = torch.exp2((100.0 * torch.arange(L, dtype=torch.float64) / n - 50).round())
+    rows = rows.view(1, 1, L, 1, 1)
+    for what, f in (("groups", groups), ("growing", rows), ("shrinking", 1 / rows),
+                    ("small", 2.0 ** -90), ("large", 2.0 ** 100)):
+        parts = base[:3] + [_times(base[3], f)]
+        _check_decode(q, parts, lens, n, what)
+    parts = [base[0], _times(base[1], 2.0 ** -70)] + base[2:]
+    _check_decode((q.double() * 2.0 ** 55).to(BF), parts, lens, n, "q", scale=2.0 ** 15 / D ** 0.5)
+
+
 @pytest.mark.parametrize("max_len", [64, 400])
 def test_decode_bad_lengths_give_zeros(cuda_lib, max_len):
     parts = _random_cache(10, 5, 2, 512, 96)

@@ -404,6 +404,48 @@ def test_binding_refuses_what_does_not_fit(cuda_lib):
     assert torch.equal(_bits(kc), _bits(c["kc"])), "a refused call wrote to the cache"
 
 
+def test_gains_that_are_parameters(cuda_lib):
+    """A model's gains require gradients: the calls read them all the same."""
+    c = _backward_case(61, 2, 6, 4, 2, 64, 128, 1)
+    kc, vc = _dev(c["kc"]), _dev(c["vc"])
+    kw = _rope_kw(c)
+    for name in ("q_gain", "k_gain"):
+        kw[name] = torch.nn.Parameter(kw[name])
+    q_out = gqa.gqa_norm_rope_append(_dev(c["q"]), _dev(c["k"]), _dev(c["v"]), kc, vc,
+                                     pos0=_dev(c["pos0"]), **kw)
+    _check_append(c, q_out, kc, vc)
+    _check_backward(c, gqa.gqa_norm_rope_append_backward(
+        _dev(c["q"]), _dev(c["k"]), _dev(c["dq_out"]), _dev(c["dkc"]), _dev(c["dvc"]),
+        pos0=_dev(c["pos0"]), **kw))
+
+
+def test_many_sequences_of_one_token(cuda_lib):
+    """More sequences than warps, with and without one to write."""
+    B = 7001
+    c = _case(62, B, 1, 2, 1, 64, 128, 2)
+    kc, vc = _dev(c["kc"]), _dev(c["vc"])
+    n_tok = (torch.arange(B) % 3 > 0).to(torch.int32)
+    before = torch.randn(B, 1, 2, 64).to(BF)
+    q_out = _dev(before)
+    new_len = torch.zeros(B, dtype=torch.int32, device=DEV)
+    gqa.gqa_norm_rope_append(_dev(c["q"]), _dev(c["k"]), _dev(c["v"]), kc, vc,
+                             pos0=_dev(c["pos0"]), n_tok=_dev(n_tok), new_len=new_len,
+                             q_out=q_out, **_rope_kw(c))
+    torch.cuda.synchronize()
+    assert torch.equal(new_len.cpu(), c["pos0"] + n_tok)
+    want, mag = _want(c, "q")
+    on = n_tok.bool()
+    _assert_rounded(q_out[on.to(DEV)], want[on], mag[on], "q")
+    assert torch.equal(_bits(q_out)[~on], _bits(before)[~on])
+    slot = torch.zeros(B, 128, dtype=torch.bool)
+    slot[torch.arange(B), c["pos0"].long()] = on
+    for got, was in ((kc, c["kc"]), (vc, c["vc"])):
+        assert torch.equal(_bits(got)[:, 0][~slot], _bits(was)[:, 0][~slot])
+    assert torch.equal(_bits(vc)[:, 0][slot], _bits(c["v"])[:, 0, 0][on])
+    want, mag = _want(c, "k")
+    _assert_rounded(kc[:, 0].cpu()[slot], want[:, 0, 0][on], mag[:, 0, 0][on], "k")
+
+
 # ---------------------------------------------------------------------------
 # as they are used: a training layer's attention, forward and backward
 # ---------------------------------------------------------------------------
