@@ -31,7 +31,7 @@
 // times the bytes that arrived, for 8 columns of work.
 //
 // Work: one CTA per (chunk of the cached slots, KV head x head subgroup, sequence).
-// Its four warps take the chunk's units of U 16-key tiles in turn, each through a ring
+// Its four warps take the chunk's units of kTiles 16-key tiles in turn, each through a ring
 // of its own (asynchronous 16-byte copies; no warp waits for another), with a
 // running softmax: the reference moves, and what is summed is scaled down, only when a
 // score passes it by more than 8, i.e. hardly ever after the first tile.  At the end
@@ -50,6 +50,9 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
+constexpr int kResident = 3;           // CTAs per SM
+constexpr int kTiles = 2;              // tiles of 16 keys that a warp takes at a time
+constexpr int kStages = 3;             // such units in a warp's ring
 constexpr int kCols = 8;               // columns of the mma: query heads of a CTA, at most
 constexpr float kSlack = 8.0f;         // a score may pass the softmax reference by this
 constexpr float kNoRef = -1e30f;       // the reference before any score: finite, so that
@@ -133,14 +136,12 @@ __device__ __forceinline__ void copy_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// U: tiles (of 16 keys) that a warp takes at a time.
-template <int D, int U>
+template <int D>
 struct DecQ4Shape {
     static constexpr int NG = Q4Shape<D>::NG;
     static constexpr int RB = D / 2;                       // bytes of codes per row
     static constexpr int SB = 4 * NG;                      // bytes of scales per row
-    static constexpr int R = 16 * U;                       // rows of a unit
-    static constexpr int kStages = U == 1 ? 4 : 3;         // units of a warp's ring
+    static constexpr int R = 16 * kTiles;                  // rows of a unit
     // Bytes from row to row in the ring.  D = 128: 80, so that neither the two rows
     // that eight lanes read of K nor the four they read of V meet in a bank.
     static constexpr int RS = D == 128 ? 80 : RB;
@@ -173,11 +174,11 @@ struct DecQ4Args {
 
 // Workspace: [(m, l): rows x 2 f32][o: rows x D f32], rows = B x Hq x n_splits, row
 // (b, h, c) = (b * Hq + h) * n_splits + c.
-template <int D, int U>
-__global__ void __launch_bounds__(kThreads, U == 1 ? 4 : 3)
+template <int D>
+__global__ void __launch_bounds__(kThreads, kResident)
 decode_q4_kernel(const DecQ4Args A) {
-    using S = DecQ4Shape<D, U>;
-    constexpr int NG = S::NG, kStages = S::kStages;
+    using S = DecQ4Shape<D>;
+    constexpr int NG = S::NG, U = kTiles;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float wml[kWarps * kCols * 2];              // (m, l) [warp][column]
     __shared__ float sw[kWarps * kCols];                   // merge weights [warp][column]
@@ -566,10 +567,10 @@ decode_q4_kernel(const DecQ4Args A) {
 }
 
 // Merges the chunks of each (sequence, query head) row.  WPR warps share a row and
-// take groups of N of its chunks in turn, lane i owning coordinates 4 i .. 4 i + 3:
+// take groups of 32 of its chunks in turn, lane i owning coordinates 4 i .. 4 i + 3:
 // all partials of a group are loaded before any is used, lane i holds chunk i's
 // (m, l), and the weights travel by shuffle.
-template <int D, int WPR, int N>
+template <int D, int WPR>
 __global__ void __launch_bounds__(128)
 decode_q4_merge_kernel(const float *__restrict__ ws_ml, const float *__restrict__ ws_o,
                        const int32_t *__restrict__ lens, int max_len, int Hq, int Lmax, int chunk,
@@ -595,11 +596,11 @@ decode_q4_merge_kernel(const float *__restrict__ ws_ml, const float *__restrict_
     const float *po = ws_o + (size_t)row * n_splits * D + lane * 4;
     float M = -INFINITY, L = 0.f;
     float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
-    for (int base = N * part; base < ns; base += N * WPR) {
-        const int n = min(N, ns - base);
-        float4 pv[N];
+    for (int base = 32 * part; base < ns; base += 32 * WPR) {
+        const int n = min(32, ns - base);
+        float4 pv[32];
 #pragma unroll
-        for (int jj = 0; jj < N; ++jj)
+        for (int jj = 0; jj < 32; ++jj)
             pv[jj] = (live && jj < n)
                          ? *reinterpret_cast<const float4 *>(po + (size_t)(base + jj) * D)
                          : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -615,7 +616,7 @@ decode_q4_merge_kernel(const float *__restrict__ ws_ml, const float *__restrict_
         a3 *= alpha;
         M = mn;
 #pragma unroll
-        for (int jj = 0; jj < N; ++jj) {
+        for (int jj = 0; jj < 32; ++jj) {
             const float wj = __shfl_sync(0xffffffffu, w, jj);
             a0 = fmaf(wj, pv[jj].x, a0);
             a1 = fmaf(wj, pv[jj].y, a1);
@@ -660,9 +661,8 @@ struct Plan {
     int G, n_sub, chunk, n_splits;
 };
 
-constexpr int kSlots = 148 * 4;        // CTAs resident at once
-constexpr int kLongChunk = 128;        // slots from which a warp takes two tiles at a time
-constexpr int kWaves = 2;              // and how many of each a full-length call should have
+constexpr int kPlaces = 148 * kResident;                   // CTAs resident at once
+constexpr double kWaves = 8.0 / 3;                         // chunks for each, see make_plan
 
 Plan make_plan(int B, int Hq, int Hkv, int max_len) {
     Plan P;
@@ -670,21 +670,23 @@ Plan make_plan(int B, int Hq, int Hkv, int max_len) {
     P.n_sub = (g + kCols - 1) / kCols;
     P.G = (g + P.n_sub - 1) / P.n_sub;
     P.n_sub = (g + P.G - 1) / P.G;
-    // Longer chunks leave less to merge, shorter ones spread a call evenly over the
-    // SMs: kWaves chunks for each place a CTA can have, of at least 64 slots (one tile
-    // for each warp).
+    // Longer chunks leave less to start up and merge, shorter ones spread a call evenly
+    // over the SMs (sequences shorter than max_len leave theirs out): kWaves chunks for
+    // each place a CTA can have, of at least 64 slots.  64 sequences of 256 .. 2048 slots
+    // take 28.7 us at 2.7 of them, 30.2 at 4, 31.2 at 5.3, 29.3 at 1; 4 of 49152 .. 65536
+    // 65.6, 65.6, 69.1, 63.5; 7 of 1 .. 1500 6.9, 8.2, 8.2, 6.8.
     const long long slots = (long long)B * Hkv * P.n_sub * max_len;
-    const long long even = (slots / (kSlots * kWaves) + 63) / 64 * 64;
+    const long long even = ((long long)((double)slots / (kPlaces * kWaves)) + 63) / 64 * 64;
     const long long most = ((long long)max_len + 63) / 64 * 64;
     P.chunk = (int)(even < 64 ? 64 : even > most ? most : even);
     P.n_splits = (max_len + P.chunk - 1) / P.chunk;
     return P;
 }
 
-template <int D, int U>
+template <int D>
 cudaError_t launch_split(const DecQ4Args &A, cudaStream_t s) {
-    using S = DecQ4Shape<D, U>;
-    auto kern = decode_q4_kernel<D, U>;
+    using S = DecQ4Shape<D>;
+    auto kern = decode_q4_kernel<D>;
     cudaLaunchAttribute pdl[1];
     pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     pdl[0].val.programmaticStreamSerializationAllowed = 1;
@@ -715,20 +717,18 @@ cudaError_t launch_split(const DecQ4Args &A, cudaStream_t s) {
 
 template <int D>
 cudaError_t launch_decode(const DecQ4Args &A, cudaStream_t s) {
-    // Two tiles at a time where each warp has several: fewer instructions a tile.
-    const cudaError_t e = A.chunk >= kLongChunk ? launch_split<D, 2>(A, s)
-                                                : launch_split<D, 1>(A, s);
+    const cudaError_t e = launch_split<D>(A, s);
     if (e != cudaSuccess || A.n_splits == 1) return e;
-    // One warp a row while a group covers its chunks, four beyond 32.
+    // One warp a row while a group covers its chunks; four beyond that (74 chunks a row,
+    // 96 rows: 66.2 us a call against 67.6 with one).
     const int rows = A.B * A.Hq;
     auto merge = [&](auto kern, int grid) {
         return launch_pdl(kern, dim3((unsigned)grid), 128, s, (const float *)A.ws_ml,
                           (const float *)A.ws_o, A.lens, A.max_len, A.Hq, A.Lmax, A.chunk,
                           A.n_splits, rows, A.out);
     };
-    if (A.n_splits > 32) return merge(decode_q4_merge_kernel<D, 4, 32>, rows);
-    if (A.n_splits > 8) return merge(decode_q4_merge_kernel<D, 1, 32>, (rows + 3) / 4);
-    return merge(decode_q4_merge_kernel<D, 1, 8>, (rows + 3) / 4);
+    return A.n_splits > 32 ? merge(decode_q4_merge_kernel<D, 4>, rows)
+                           : merge(decode_q4_merge_kernel<D, 1>, (rows + 3) / 4);
 }
 
 // ---------------------------------------------------------------------------

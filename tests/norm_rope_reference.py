@@ -139,8 +139,8 @@ def decode(q, cache, lens, scale=None):
         the score in the scaling and the exponential;
       * that moves p by up to 2 d of itself in numerator and denominator together;
       * p s is rounded once to fp16, 2^-12 of each product p s c with c <= 15; additions
-        over at most 64 keys of a warp and the merges within 80 U32 of
-        sum p (15 s + |m|);
+        over the keys of a warp (at most 64 at the tests' sizes) and the merges within
+        80 U32 of sum p (15 s + |m|);
       * the result's rounding to bf16, 2^-8 of it."""
     kc, ks, vc, vs = cache
     B, Hq, D = q.shape
