@@ -24,6 +24,9 @@ namespace gqa {
 namespace {
 
 constexpr int kWarps = 4;              // warps per CTA
+// Measured on 8 x 2048 tokens of 24 / 8 heads, D = 128 (335 MB, 51 us at the copy rate):
+// 62 us, 82 % of it; rings of 2, 4 and 8 passes 71, 65 and 64 us (longer ones leave less
+// L1 for positions), 6 CTAs an SM 65 us.
 constexpr int kResident = 5;           // CTAs per SM
 constexpr int kRing = 3;               // passes on their way or waiting, per warp
 
@@ -261,7 +264,8 @@ norm_rope_append_kernel(const AppendArgs A, const __grid_constant__ RopeTable ta
                 end_ahead = is_q ? qp : is_k ? qp + kp : npass;
                 const int h = (ps_ahead - (is_q ? 0 : is_k ? qp : qp + kp)) * S::kVecPerWarp + slot;
                 const int heads = is_q ? A.Hq : A.Hkv;
-                src = (is_q ? A.q : is_k ? A.k : A.v) + (((size_t)ahead.b * A.T + ahead.t) * heads + h) * D + 8 * j;
+                const size_t tok = (size_t)ahead.b * A.T + ahead.t;
+                src = (is_q ? A.q : is_k ? A.k : A.v) + (tok * heads + h) * D + 8 * j;
                 left_ahead = active ? heads - h : 0;
             }
             if (left_ahead > 0) {
@@ -371,10 +375,13 @@ norm_rope_append_kernel(const AppendArgs A, const __grid_constant__ RopeTable ta
 // Bound by memory: x, dy read once and dx written once.  The loads go through rings as
 // in the forward.  A CTA takes either query passes or key and value passes, of tokens
 // (or slices of them) in turn, so that a lane keeps one gain and the sums of one gain's
-// gradient, for its 16 coordinates, in registers over all its units; the CTAs are
-// shared out by the bytes of the two.  At the end a CTA adds its warps' sums and leaves
-// one row in the workspace, and a second kernel adds the rows in a fixed order, so
-// equal calls give equal bits.
+// gradient, for its 16 coordinates, in registers over all its units.  At the end a CTA
+// adds its warps' sums and leaves one row in the workspace, and a second kernel adds the
+// rows in a fixed order, so equal calls give equal bits.
+//
+// Measured on 8 x 2048 tokens of 24 / 8 heads, D = 128 (470 MB, 72 us at the copy rate):
+// 81 us, 88 % of it; 4 CTAs an SM at fewer registers 97 us; 3 x 1001 tokens of 8 / 8
+// heads, D = 96 (5.6 us) 16.8 us, 3 of them the second kernel.
 constexpr int kBwdWarps = 4;
 constexpr int kBwdResident = 3;                            // CTAs per SM
 constexpr int kBwdMaxCtas = 148 * kBwdResident;
@@ -655,7 +662,8 @@ gain_sum_kernel(const float *__restrict__ partial, int n_q, int n_rows, int D, f
     }
 }
 
-// Slices of a token's passes: one, unless the tokens alone leave most warps idle.
+// Slices of a token's passes: one, unless the tokens alone leave most warps idle (64
+// single tokens: 4.7 us against 7.2 unsliced; 16384 tokens: 62 us against 77 in two).
 int slices(long long tokens, int npass, int warps) {
     const long long want = (warps + tokens - 1) / tokens;
     return (int)(want < 1 ? 1 : want > npass ? npass : want);
@@ -697,8 +705,9 @@ cudaError_t launch_backward(BackwardArgs A, const gqa_rope_params &p, const gqa_
         const long long need = (tokens * A.slices[i] + kBwdWarps - 1) / kBwdWarps;
         return (int)(need < n_ctas ? need : n_ctas);
     };
-    // CTAs in that proportion.  With few tokens a warp the last, partly filled round counts:
-    // the best of the shares around it by the longer role's rounds.
+    // CTAs in that proportion (87 us for 8 x 2048 tokens; by the rows moved 94).  With few
+    // tokens a warp the last, partly filled round counts: the best of the shares around it
+    // by the longer role's rounds (3 x 1001 tokens: 16.8 us against 18.8).
     const int even = (int)(kBwdMaxCtas * cost[0] / (cost[0] + cost[1]) + 0.5);
     int best = even;
     if (tokens < 16LL * kBwdMaxCtas * kBwdWarps) {
@@ -754,7 +763,8 @@ gqa_status check_append(const void *q, const void *k, const void *v, const void 
     if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) ||
         !aligned4(pos0) || !aligned4(n_tok) || !aligned4(new_len))
         return GQA_ERR_INVALID_ARG;
-    if (new_len && (new_len == pos0 || new_len == n_tok)) return GQA_ERR_INVALID_ARG;
+    auto overlaps = [&](const int32_t *a) { return a && new_len < a + B && a < new_len + B; };
+    if (new_len && (overlaps(pos0) || overlaps(n_tok))) return GQA_ERR_INVALID_ARG;
     if (!params_ok(p)) return GQA_ERR_INVALID_ARG;
     if (!head_dim_ok(D)) return GQA_ERR_UNSUPPORTED;
     if (!inputs_ok(x, p, D)) return GQA_ERR_INVALID_ARG;

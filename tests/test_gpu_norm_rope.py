@@ -6,6 +6,8 @@ products and a sum, fp32 sines of angles reduced in float64: some tens of fp32 u
 the magnitude |a| + |b| of its pair -- and rounded once to bf16: half a step, 2^-8 of the
 value.  A gradient element likewise, with the magnitudes of its two terms.
 """
+from types import SimpleNamespace
+
 import pytest
 import torch
 
@@ -391,6 +393,9 @@ def test_binding_refuses_what_does_not_fit(cuda_lib):
     lens = torch.zeros(2, dtype=torch.int32, device=DEV)
     with pytest.raises(gqa.GqaError):
         gqa.gqa_norm_rope_append(**dict(good, pos0=lens, new_len=lens))
+    other = SimpleNamespace(device=torch.device("cuda", 1), cuda_stream=0)
+    with pytest.raises(ValueError, match="stream"):
+        gqa.gqa_norm_rope_append(**dict(good, q_out=torch.empty_like(q), stream=other))
     dkc = torch.zeros_like(kc)
     with pytest.raises(gqa.GqaError):
         gqa.gqa_norm_rope_append_backward(q, k, q, dkc, dkc, workspace=torch.empty(

@@ -75,7 +75,7 @@ def test_quantiser_ties_constants_and_values_that_are_not_finite():
 F = ctypes.c_void_p(0x10000)
 ODD = ctypes.c_void_p(0x10008)             # not 16-byte aligned
 ODD4 = ctypes.c_void_p(0x10002)            # not 4-byte aligned
-OTHER = ctypes.c_void_p(0x20000)
+NEXT = ctypes.c_void_p(0x10004)            # one int32 on
 NORM = _lib.RopeParams(1, 1e-6, 10000.0)
 PLAIN = _lib.RopeParams(0, 1e-6, 10000.0)
 
@@ -105,6 +105,7 @@ APPEND_REFUSED = [
     (1, dict(L=100)), (1, dict(L=0)), (2, dict(D=80)), (2, dict(D=0)),
     (3, dict(T=129)), (3, dict(max_pos0=113)), (3, dict(n_tok=F, max_pos0=129)),
     (1, dict(pos0=F, new_len=F)), (1, dict(n_tok=F, new_len=F)),
+    (1, dict(pos0=F, new_len=NEXT, B=2)), (1, dict(n_tok=NEXT, new_len=F, B=2)),
     (1, dict(p=_lib.RopeParams(1, -1.0, 10000.0))), (1, dict(p=_lib.RopeParams(1, 1e-6, 1.0))),
     (1, dict(p=PLAIN, x=_inputs(q_gain=0x10000))), (1, dict(p=PLAIN, x=_inputs(k_gain=0x10000))),
     (1, dict(x=_inputs(q_gain=0x10008))), (1, dict(x=_inputs(pos=0x10002))),
