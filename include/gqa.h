@@ -432,8 +432,8 @@ gqa_status kv_cache_read_q4(const void *k_codes, const void *k_scales, const voi
 /*
  * gqa_decode_q4 -- gqa_decode against a 4-bit cache; K and V are the values
  * m + s c, not rounded to bf16.  Lengths, errors and the workspace's rules as
- * there; gqa_decode_q4_workspace_bytes gives its size (where one chunk covers
- * max_len_host nothing is merged and no workspace is used; 16 bytes are named then).
+ * there; gqa_decode_q4_workspace_bytes gives its size (16 bytes are named for calls
+ * that merge without it: one chunk, or few and short rows).
  * The chunks' length follows from B, the heads and max_len_host.  Queries and values
  * of magnitude up to 2^60 and 2^110 are handled (sums of larger ones can overflow).
  */

@@ -38,6 +38,9 @@
 // the warps' statistics and partial outputs are merged in shared memory, the chunk's
 // (m, l, o) goes to the workspace and a second kernel, a programmatic dependent,
 // merges the chunks.  When one chunk covers max_len the CTA writes the output itself.
+// Calls of few, short rows (make_plan) merge without a second kernel: a row's CTAs are a
+// thread-block cluster, each hands its (m, l, o) to the first one's shared memory, and
+// that one writes the output.
 #include <atomic>
 #include <type_traits>
 
@@ -54,6 +57,7 @@ constexpr int kResident = 3;           // CTAs per SM
 constexpr int kTiles = 2;              // tiles of 16 keys that a warp takes at a time
 constexpr int kStages = 3;             // such units in a warp's ring
 constexpr int kCols = 8;               // columns of the mma: query heads of a CTA, at most
+constexpr int kMaxCluster = 8;         // CTAs of a cluster
 constexpr float kSlack = 8.0f;         // a score may pass the softmax reference by this
 constexpr float kNoRef = -1e30f;       // the reference before any score: finite, so that
                                        // 2^(a score of -inf - it) is 0
@@ -125,6 +129,22 @@ __device__ __forceinline__ void load_words(uint32_t (&w)[NG], const uint32_t *p)
     }
 }
 
+// Cluster: the barrier, and stores to the first CTA's shared memory.
+__device__ __forceinline__ void cluster_arrive() {
+    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t in_first_cta(uint32_t smem) {
+    uint32_t a;
+    asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(smem));
+    return a;
+}
+__device__ __forceinline__ void store_remote(uint32_t at, float x, float y) {
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(at), "f"(x), "f"(y) : "memory");
+}
+
 // 16 bytes, global to shared, the last 16 - n of them zeros; counted by commit groups.
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src, int n = 16) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
@@ -157,6 +177,10 @@ struct DecQ4Shape {
     static constexpr int kPartStride = D + 4;
     static constexpr int kPart = kWarps * kCols * kPartStride * 4;
     static constexpr int kSmem = kRing > kPart ? kRing : kPart;
+    // Clusters: what each CTA hands to the first one, over its ring: o [kCols][D],
+    // (m, l) [kCols].
+    static constexpr int kGather = kCols * (D + 2) * 4;
+    static_assert(kMaxCluster * kGather <= kSmem, "the parts of a cluster fit over a ring");
 };
 
 struct DecQ4Args {
@@ -169,12 +193,13 @@ struct DecQ4Args {
     int32_t *status;
     int max_len, B, Hq, Hkv, Lmax, n_sub, G;               // G: query heads per CTA
     int chunk, n_splits;                                   // slots per CTA, chunks of max_len
+    int cluster;                                           // CTAs of a row's cluster, or 0
     float scale_log2;                  // 2^69 scale / ln 2: the scores come in units of 2^-69
 };
 
 // Workspace: [(m, l): rows x 2 f32][o: rows x D f32], rows = B x Hq x n_splits, row
 // (b, h, c) = (b * Hq + h) * n_splits + c.
-template <int D>
+template <int D, bool CLUSTER>
 __global__ void __launch_bounds__(kThreads, kResident)
 decode_q4_kernel(const DecQ4Args A) {
     using S = DecQ4Shape<D>;
@@ -201,12 +226,20 @@ decode_q4_kernel(const DecQ4Args A) {
     if (len < 1 || len > A.max_len || len > A.Lmax) {
         if (c == 0 && blockIdx.x == 0 && tid == 0)
             report(A.status, len < 1 ? GQA_DEV_BAD_LEN : GQA_DEV_CAPACITY);
-        if (A.n_splits == 1)
+        if (A.n_splits == 1 || (CLUSTER && c == 0))
             for (int i = tid; i < G * D; i += kThreads) A.out[((size_t)b * A.Hq + h0) * D + i] = 0;
         return;
     }
     const int key0 = c * A.chunk;
-    if (key0 >= len) return;
+    if (key0 >= len) {
+        if constexpr (CLUSTER) {                           // (len is the whole cluster's)
+            cluster_arrive();
+            cluster_wait();
+            cluster_arrive();
+            cluster_wait();
+        }
+        return;
+    }
     const int nk = min(A.chunk, len - key0);
 
     // ---- the warp's ring ----
@@ -538,30 +571,80 @@ decode_q4_kernel(const DecQ4Args A) {
             L = fmaf(f, wml[(w * kCols + tid) * 2 + 1], L);
         }
         s_inv[tid] = 1.f / L;
-        if (A.n_splits > 1) {
+        if constexpr (CLUSTER) {
+            wml[2 * tid] = M;
+            wml[2 * tid + 1] = L;
+        } else if (A.n_splits > 1) {
             A.ws_ml[(row0 + (size_t)tid * A.n_splits) * 2] = M;
             A.ws_ml[(row0 + (size_t)tid * A.n_splits) * 2 + 1] = L;
         }
     }
     __syncthreads();
-    for (int idx = tid; idx < G * (D / 2); idx += kThreads) {
-        const int h = idx / (D / 2), d = 2 * (idx - h * (D / 2));
-        float a0 = 0.f, a1 = 0.f;
+    constexpr int kPer = kCols * (D / 2) / kThreads;       // pairs of coordinates per thread
+    float2 sum[kPer];
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            const float f = sw[w * kCols + h];
-            const float2 v =
-                *reinterpret_cast<const float2 *>(part + (w * kCols + h) * S::kPartStride + d);
-            a0 = fmaf(f, v.x, a0);
-            a1 = fmaf(f, v.y, a1);
+    for (int i = 0; i < kPer; ++i) {
+        const int idx = tid + i * kThreads;
+        const int h = idx / (D / 2), d = 2 * (idx - h * (D / 2));
+        sum[i] = make_float2(0.f, 0.f);
+        if (h < G) {
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float f = sw[w * kCols + h];
+                const float2 v =
+                    *reinterpret_cast<const float2 *>(part + (w * kCols + h) * S::kPartStride + d);
+                sum[i].x = fmaf(f, v.x, sum[i].x);
+                sum[i].y = fmaf(f, v.y, sum[i].y);
+            }
         }
-        if (A.n_splits == 1) {
-            const float inv = s_inv[h];
+    }
+    uint32_t hand = 0;                                     // this CTA's place in the first one
+    if constexpr (CLUSTER) {
+        cluster_arrive();                                  // no CTA needs its ring any more
+        cluster_wait();
+        hand = in_first_cta(ptx::smem_addr(smem) + c * S::kGather);
+        if (tid < G) store_remote(hand + kCols * D * 4 + 8 * tid, wml[2 * tid], wml[2 * tid + 1]);
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int idx = tid + i * kThreads;
+        const int h = idx / (D / 2), d = 2 * (idx - h * (D / 2));
+        if (h < G) {
+            if constexpr (CLUSTER) {
+                store_remote(hand + (h * D + d) * 4, sum[i].x, sum[i].y);
+            } else if (A.n_splits == 1) {
+                const float inv = s_inv[h];
+                *reinterpret_cast<uint32_t *>(A.out + ((size_t)b * A.Hq + h0 + h) * D + d) =
+                    pack_bf16x2(sum[i].x * inv, sum[i].y * inv);
+            } else {
+                *reinterpret_cast<float2 *>(A.ws_o + (row0 + (size_t)h * A.n_splits) * D + d) =
+                    sum[i];
+            }
+        }
+    }
+    if constexpr (CLUSTER) {
+        cluster_arrive();
+        cluster_wait();
+        if (c != 0) return;
+        const int n = (len + A.chunk - 1) / A.chunk;
+        const float *got = reinterpret_cast<const float *>(smem);
+        constexpr int kFloats = S::kGather / 4;
+        for (int idx = tid; idx < G * (D / 2); idx += kThreads) {
+            const int h = idx / (D / 2), d = 2 * (idx - h * (D / 2));
+            const float *ml = got + kCols * D + 2 * h;
+            float M = ml[0];
+            for (int i = 1; i < n; ++i) M = fmaxf(M, ml[i * kFloats]);
+            float L = 0.f, a0 = 0.f, a1 = 0.f;
+            for (int i = 0; i < n; ++i) {
+                const float f = ex2(ml[i * kFloats] - M);
+                const float2 v = *reinterpret_cast<const float2 *>(got + i * kFloats + h * D + d);
+                L = fmaf(f, ml[i * kFloats + 1], L);
+                a0 = fmaf(f, v.x, a0);
+                a1 = fmaf(f, v.y, a1);
+            }
+            const float inv = 1.f / L;
             *reinterpret_cast<uint32_t *>(A.out + ((size_t)b * A.Hq + h0 + h) * D + d) =
                 pack_bf16x2(a0 * inv, a1 * inv);
-        } else {
-            *reinterpret_cast<float2 *>(A.ws_o + (row0 + (size_t)h * A.n_splits) * D + d) =
-                make_float2(a0, a1);
         }
     }
 }
@@ -658,9 +741,17 @@ decode_q4_merge_kernel(const float *__restrict__ ws_ml, const float *__restrict_
 
 // How a call is cut: heads per CTA, slots per chunk, chunks of a sequence.
 struct Plan {
-    int G, n_sub, chunk, n_splits;
+    int G, n_sub, chunk, n_splits, cluster;
 };
 
+// Calls without a second kernel ask for so much shared memory that an SM takes two CTAs,
+// which spreads their few CTAs evenly: 288 of 1024 slots (18 sequences of 2048) take 13.6 us,
+// with three on some SMs 17.7.  Against the form with a second kernel: 1 x 612 slots 3.9
+// us against 4.5 (and one launch less for the host: 5.1 against 7.4), 16 x 600 slots of 8
+// KV heads 7.7 against 11.7, 18 x 2048 13.6 against 17.9.
+constexpr int kWideSmem = 100 * 1024;
+constexpr int kClusterPlaces = 148 * 2;
+constexpr int kClusterLen = 4096;      // longer rows want more than eight chunks
 constexpr int kPlaces = 148 * kResident;                   // CTAs resident at once
 constexpr double kWaves = 8.0 / 3;                         // chunks for each, see make_plan
 
@@ -670,11 +761,28 @@ Plan make_plan(int B, int Hq, int Hkv, int max_len) {
     P.n_sub = (g + kCols - 1) / kCols;
     P.G = (g + P.n_sub - 1) / P.n_sub;
     P.n_sub = (g + P.G - 1) / P.G;
+    P.cluster = 0;
+    // Few, short rows: one to eight chunks of at least 64 slots, merged within a cluster, as
+    // long as all CTAs have a place at once (clusters of eight find only half of them: 32 of
+    // them took 8.4 us on 4 x 1000 slots of 8 KV heads, of four 5.5) and long chunks fill
+    // the places (96 rows of 4096 slots in 192 CTAs 22.5 us, cut finer 18.3).
+    const long long rows = (long long)B * Hkv * P.n_sub;
+    if (max_len <= kClusterLen && rows <= kClusterPlaces) {
+        int c = 1;
+        while (c < kMaxCluster && 64 * c < max_len &&
+               2 * c * rows <= (2 * c < 8 ? kClusterPlaces : kClusterPlaces / 2))
+            c *= 2;
+        P.chunk = ((max_len + c - 1) / c + 63) / 64 * 64;
+        P.n_splits = (max_len + P.chunk - 1) / P.chunk;
+        P.cluster = c > 1 ? c : 0;                         // one chunk needs none
+        if (P.chunk <= 1024 || 8 * c * rows >= 7 * kClusterPlaces) return P;
+        P.cluster = 0;
+    }
     // Longer chunks leave less to start up and merge, shorter ones spread a call evenly
     // over the SMs (sequences shorter than max_len leave theirs out): kWaves chunks for
     // each place a CTA can have, of at least 64 slots.  64 sequences of 256 .. 2048 slots
     // take 28.7 us at 2.7 of them, 30.2 at 4, 31.2 at 5.3, 29.3 at 1; 4 of 49152 .. 65536
-    // 65.6, 65.6, 69.1, 63.5; 7 of 1 .. 1500 6.9, 8.2, 8.2, 6.8.
+    // 65.6, 65.6, 69.1, 63.5.
     const long long slots = (long long)B * Hkv * P.n_sub * max_len;
     const long long even = ((long long)((double)slots / (kPlaces * kWaves)) + 63) / 64 * 64;
     const long long most = ((long long)max_len + 63) / 64 * 64;
@@ -683,20 +791,24 @@ Plan make_plan(int B, int Hq, int Hkv, int max_len) {
     return P;
 }
 
-template <int D>
+template <int D, bool CLUSTER>
 cudaError_t launch_split(const DecQ4Args &A, cudaStream_t s) {
     using S = DecQ4Shape<D>;
-    auto kern = decode_q4_kernel<D>;
-    cudaLaunchAttribute pdl[1];
-    pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    pdl[0].val.programmaticStreamSerializationAllowed = 1;
+    auto kern = decode_q4_kernel<D, CLUSTER>;
+    static_assert(kWideSmem >= S::kSmem, "rings");
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = (unsigned)A.cluster;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(A.Hkv * A.n_sub, A.B, A.n_splits);
+    cfg.gridDim = dim3(A.Hkv * A.n_sub, A.B, CLUSTER ? A.cluster : A.n_splits);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = S::kSmem;
+    cfg.dynamicSmemBytes = CLUSTER || A.n_splits == 1 ? kWideSmem : S::kSmem;
     cfg.stream = s;
-    cfg.attrs = pdl;
-    cfg.numAttrs = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = CLUSTER ? 2 : 1;
     // The kernel's limit of shared memory is raised once per device; a context that does
     // not know of it yet refuses the launch.
     static std::atomic<uint64_t> raised{0};
@@ -709,7 +821,7 @@ cudaError_t launch_split(const DecQ4Args &A, cudaStream_t s) {
         if (e != cudaErrorInvalidValue) return e;
         cudaGetLastError();
     }
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kWideSmem);
     if (e != cudaSuccess) return e;
     raised.fetch_or(bit, std::memory_order_relaxed);
     return cudaLaunchKernelEx(&cfg, kern, A);
@@ -717,7 +829,8 @@ cudaError_t launch_split(const DecQ4Args &A, cudaStream_t s) {
 
 template <int D>
 cudaError_t launch_decode(const DecQ4Args &A, cudaStream_t s) {
-    const cudaError_t e = launch_split<D>(A, s);
+    if (A.cluster) return launch_split<D, true>(A, s);
+    const cudaError_t e = launch_split<D, false>(A, s);
     if (e != cudaSuccess || A.n_splits == 1) return e;
     // One warp a row while a group covers its chunks; four beyond that (74 chunks a row,
     // 96 rows: 66.2 us a call against 67.6 with one).
@@ -864,7 +977,7 @@ extern "C" size_t gqa_decode_q4_workspace_bytes(int B, int Hq, int Hkv, int D, i
     if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || max_len < 1 || !gqa_host::head_dim_ok(D))
         return 0;
     const gqa::Plan P = gqa::make_plan(B, Hq, Hkv, max_len);
-    if (P.n_splits == 1) return 16;                        // the chunk's CTA writes the output
+    if (P.n_splits == 1 || P.cluster) return 16;           // no second kernel: not used
     const size_t rows = (size_t)B * Hq * P.n_splits;
     // The partial outputs start on a 16-byte boundary.
     return (rows * 2 * 4 + 15) / 16 * 16 + rows * (size_t)D * 4;
@@ -889,7 +1002,7 @@ extern "C" gqa_status gqa_decode_q4(const void *q, const void *k_codes, const vo
     if (max_len_host > Lmax) return GQA_ERR_CAPACITY;
     const size_t need = gqa_decode_q4_workspace_bytes(B, Hq, Hkv, D, max_len_host);
     const gqa::Plan P = gqa::make_plan(B, Hq, Hkv, max_len_host);
-    if (P.n_splits > 1 && (!ws || ws_bytes < need || !aligned16(ws))) return GQA_ERR_WORKSPACE;
+    if (!ws || ws_bytes < need || !aligned16(ws)) return GQA_ERR_WORKSPACE;
     gqa::DecQ4Args A = {};
     A.q = static_cast<const uint16_t *>(q);
     A.kc = static_cast<const uint8_t *>(k_codes);
@@ -909,6 +1022,7 @@ extern "C" gqa_status gqa_decode_q4(const void *q, const void *k_codes, const vo
     A.Lmax = Lmax;
     A.n_splits = P.n_splits;
     A.chunk = P.chunk;
+    A.cluster = P.cluster;
     A.n_sub = P.n_sub;
     A.G = P.G;
     A.scale_log2 = (scale > 0.f ? scale : 1.0f / sqrtf((float)D)) * 1.4426950408889634f * 0x1p69f;

@@ -157,10 +157,11 @@ def test_read_refusals(lib, want, over):
 @pytest.mark.parametrize("want,over", [
     (1, dict(q=None)), (1, dict(q=ODD)), (1, dict(c=ODD)), (1, dict(lens=None)),
     (1, dict(lens=ODD4)), (1, dict(Hq=5)), (1, dict(B=70000)), (2, dict(D=72)),
-    (1, dict(L=200)), (1, dict(n=0)), (3, dict(n=2049)), (6, dict(ws=None)),
+    (1, dict(L=200)), (1, dict(n=0)), (3, dict(n=4097)), (6, dict(ws=None)),
+    (6, dict(ws=None, n=1)), (6, dict(ws=None, n=300)), (6, dict(ws_bytes=15, n=300)),
     (6, dict(ws_bytes=16)), (6, dict(ws=ODD))])
 def test_decode_q4_refusals(lib, want, over):
-    d = dict(q=F, c=F, lens=F, n=2000, Hq=4, B=1, D=64, L=2048, ws=F, ws_bytes=1 << 24)
+    d = dict(q=F, c=F, lens=F, n=4000, Hq=4, B=1, D=64, L=4096, ws=F, ws_bytes=1 << 24)
     d.update(over)
     assert lib.gqa_decode_q4(d["q"], d["c"], F, F, F, d["lens"], d["n"], F, d["B"], d["Hq"], 2,
                              d["D"], d["L"], 0.0, d["ws"], d["ws_bytes"], None, None) == want
@@ -173,6 +174,7 @@ def test_workspace_sizes(lib):
     assert f(0, 4, 2, 64, 100) == 0 and f(1, 5, 2, 64, 100) == 0 and f(1, 4, 2, 80, 100) == 0
     assert f(1, 4, 2, 64, 0) == 0
     assert f(1, 4, 2, 64, 1) == 16             # one chunk: no partials
+    assert f(1, 4, 2, 64, 1000) == 16          # few, short rows: merged on the chip
     # whatever the cut: one to max_len / 64 rows of D + 2 floats per query head
     row = 64 * 24 * 130 * 4
     assert 2 * row <= f(64, 24, 8, 128, 2049) <= 33 * row + 16
