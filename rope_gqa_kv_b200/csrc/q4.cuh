@@ -7,7 +7,7 @@
 // stands for m + s c:
 //     m = min x,   s = bf16((max x - m) / 15),   c = ceil((x - m) / s - 1/2).
 // The values quantised are bf16, so m is exact; rounding s to 8 bits moves the
-// largest value's quotient by at most 15 * 2^-9 = 0.03, so no code is clipped and
+// largest value's quotient by at most 15 * 2^-8 = 0.06, so no code is clipped and
 // |m + s c - x| <= s/2 holds for every value.  A group with s below 2^-126 keeps
 // s = 0 (all values m); one that holds a value that is not finite keeps m = NaN,
 // s = 0: all its values read back as NaN.

@@ -138,7 +138,9 @@ def decode(q, cache, lens, scale=None):
         sum |q| (15 s + |m|), so off by d = 36 U32 A_q scale, and a few fp32 units of
         the score in the scaling and the exponential;
       * that moves p by up to 2 d of itself in numerator and denominator together;
-      * p s is rounded once to fp16, 2^-12 of each product p s c with c <= 15; additions
+      * p s is rounded once to fp16 (11 significant bits: half a step is 2^-11 of the
+        value, torch.finfo(torch.float16).eps / 2), 2^-11 of each product p s c with
+        c <= 15; additions
         over the keys of a warp (at most 64 at the tests' sizes) and the merges within
         80 U32 of sum p (15 s + |m|);
       * the result's rounding to bf16, 2^-8 of it."""
@@ -161,7 +163,7 @@ def decode(q, cache, lens, scale=None):
             mag = x.abs() @ (15 * s_k + m_k.abs()).T * scale
             d = (36 * U32 * mag + 8 * U32 * (sc.abs() + 1)).amax(-1, keepdim=True)
             s_v, m_v = vs[b, h, :n].to(F64)[..., 0][:, grp], vs[b, h, :n].to(F64)[..., 1][:, grp]
-            e = 2 * d * (p @ V.abs()) + 2.0 ** -12 * 15 * (p @ s_v)
+            e = 2 * d * (p @ V.abs()) + 2.0 ** -11 * 15 * (p @ s_v)
             e = e + 80 * U32 * (p @ (15 * s_v + m_v.abs()))
             out[b, h * g:(h + 1) * g] = o
             tol[b, h * g:(h + 1) * g] = 2.0 ** -8 * o.abs() + 1.01 * e
