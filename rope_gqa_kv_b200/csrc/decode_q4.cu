@@ -23,7 +23,7 @@
 //   * output: sum_k p_k (m_k + s_k c_k,d).  p_k s_k is the 8-column operand, carried
 //     by movmatrix from the score layout, in fp16 after a power of two that brings the
 //     group's largest s so far to 2^5 .. 2^6: one rounding, 2^-11 of the term, against
-//     bf16's 2^-8 (terms below 2^-20 of the group's largest lose bits, 2^-31 of it at
+//     bf16's 2^-8 (terms below 2^-19 of the group's largest lose bits, 2^-30 of it at
 //     most).
 //     sum(p m) is added up in fp32 beside it.
 // mma.sync rather than tcgen05: its operands come from registers, where the codes
