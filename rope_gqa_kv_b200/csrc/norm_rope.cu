@@ -402,11 +402,13 @@ struct BackwardArgs {
 };
 
 // One vector: dx of the lane's 16 coordinates in place of dy (ya, yb), and its share of
-// d gain added to dg.  Lanes without a vector hold zeros.
+// d gain added to dg.  Lanes without a vector (live false) hold zeros and take r = 0: with
+// eps = 0 their r would be infinite and their share of d gain NaN.
 template <int D>
 __device__ __forceinline__ void backward_vector(const uint4 xa, const uint4 xb, uint4 &ya,
                                                 uint4 &yb, const float (&c)[8],
-                                                const float (&s)[8], bool qk_norm, float eps,
+                                                const float (&s)[8], bool live, bool qk_norm,
+                                                float eps,
                                                 const float (&gain)[16], float (&dg)[16]) {
     using S = RopeShape<D>;
     const uint32_t xw[8] = {xa.x, xa.y, xa.z, xa.w, xb.x, xb.y, xb.z, xb.w};
@@ -434,7 +436,7 @@ __device__ __forceinline__ void backward_vector(const uint4 xa, const uint4 xb, 
         }
         const float ss = group_sum<S::kTPV>(ss0 + ss1);
         const float xz = group_sum<S::kTPV>(xz0 + xz1);
-        const float r = rsqrtf(ss * (1.0f / D) + eps);
+        const float r = live ? rsqrtf(ss * (1.0f / D) + eps) : 0.f;
         const float k = -r * (xz * r * (1.0f / D));        // r^3 alone could overflow
 #pragma unroll
         for (int e = 0; e < 16; e += 2) {
@@ -589,7 +591,8 @@ __device__ __forceinline__ void backward_units(const BackwardArgs &A, const Rope
             }
             load_next(stage == 0 ? kBwdRing - 1 : stage - 1);
             stage = stage == kBwdRing - 1 ? 0 : stage + 1;
-            if (!value) backward_vector<D>(xa, xb, ya, yb, c, s, norm, A.eps, gain, dg);
+            if (!value)
+                backward_vector<D>(xa, xb, ya, yb, c, s, left > 0, norm, A.eps, gain, dg);
             if (left > 0) {
                 *reinterpret_cast<uint4 *>(dst) = ya;
                 *reinterpret_cast<uint4 *>(dst + S::kHalf) = yb;

@@ -288,6 +288,30 @@ def test_backward_without_a_gain_or_the_norm(cuda_lib, gains):
     _check_backward(c, got, qk_norm=False)
 
 
+@pytest.mark.parametrize("D", [64, 96, 128])
+def test_backward_without_eps(cuda_lib, D):
+    """eps = 0 with head counts that leave some of a warp's places empty: the gains'
+    gradients stay those of the vectors that are there."""
+    c = _backward_case(24, 2, 13, 6, 3, D, 128, 1)
+    with_eps = _run_backward(c)
+    got = _run_backward(c, eps=0.0)
+    # 1e-6 next to a mean square of about 1 moves r by 5e-7 of itself, four roundings' worth,
+    # and the gains' sums by that and the bounds of _check_backward twice over
+    for i, name in enumerate("qk"):
+        x, dy = c[name].double(), (c["dq_out"] if i == 0 else _slots(c, c["dkc"])).double()
+        r = 1 / torch.sqrt((x * x).mean(-1, keepdim=True))
+        n = 2 * 13 * c[name].shape[2]
+        allow = (2 * (n + 64) * 2.0 ** -24 + 1e-6 * float((r * r).max())) * (
+            _pair_mag(dy) * x.abs() * r).sum(dim=(0, 1, 2))
+        d = (got[3 + i].double() - with_eps[3 + i].double()).abs().cpu()
+        assert (d <= allow).all(), (name, float((d / allow).max()))
+        P = ref.positions(c["pos0"], 2, 13, c["pos"], c["pair_axis"], D)
+        dx, _ = ref.norm_rope_grad(x, dy, P, c[name + "_gain"], True, eps=0.0)
+        gm = c[name + "_gain"].double().abs() * _pair_mag(dy)
+        mag = r * gm + x.abs() * r ** 3 * (x.abs() * gm).mean(-1, keepdim=True)
+        _assert_rounded(got[i], dx, mag, "d" + name)
+
+
 def test_backward_against_differences(cuda_lib):
     """sum(grad . u) against the central difference of the float64 forward along u.  The
     kernel's dx are rounded: the sum may be off by 2^-8 of sum |dx u| (and far less)."""
