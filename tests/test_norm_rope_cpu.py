@@ -159,7 +159,7 @@ def test_read_refusals(lib, want, over):
     (1, dict(lens=ODD4)), (1, dict(Hq=5)), (1, dict(B=70000)), (2, dict(D=72)),
     (1, dict(L=200)), (1, dict(n=0)), (3, dict(n=4097)), (6, dict(ws=None)),
     (6, dict(ws=None, n=1)), (6, dict(ws=None, n=300)), (6, dict(ws_bytes=15, n=300)),
-    (6, dict(ws_bytes=16)), (6, dict(ws=ODD))])
+    (6, dict(ws_bytes=16, n=5000, L=8192)), (6, dict(ws=ODD))])
 def test_decode_q4_refusals(lib, want, over):
     d = dict(q=F, c=F, lens=F, n=4000, Hq=4, B=1, D=64, L=4096, ws=F, ws_bytes=1 << 24)
     d.update(over)
