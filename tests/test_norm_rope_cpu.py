@@ -226,3 +226,12 @@ def test_native_argument_checks_leave_host_tensors_to_the_slow_path(lib):
     for bad in ((0,), (0, ("t", t)), ("x", ()), (0, ["t", t, None, None])):
         with pytest.raises(TypeError):
             _fastargs.pointers(*bad)
+
+
+def test_parameters_follow_a_value_that_changes_in_place():
+    """eps and rope_base may be anything float() takes; none is kept by its identity."""
+    eps = torch.tensor(1e-6)
+    first = _lib._params_bytes(True, eps, 1e4, None)
+    eps.fill_(0.5)
+    assert _lib._params_bytes(True, eps, 1e4, None) != first
+    assert _lib._params(True, eps, 1e4).eps == 0.5
