@@ -342,9 +342,9 @@ def _rope_inputs(q_gain, k_gain, pos, axes):
     return x
 
 
-@functools.lru_cache(maxsize=64)
+@functools.lru_cache(maxsize=64)       # of plain numbers: nothing is kept by an object's identity
 def _plain_params(qk_norm, eps, rope_base):
-    return RopeParams(1 if qk_norm else 0, float(eps), float(rope_base))
+    return RopeParams(qk_norm, eps, rope_base)
 
 
 @functools.lru_cache(maxsize=64)
@@ -354,13 +354,13 @@ def _plain_params_bytes(qk_norm, eps, rope_base):
 
 def _params_bytes(qk_norm, eps, rope_base, scaling):
     if scaling is None:
-        return _plain_params_bytes(qk_norm, eps, rope_base)
+        return _plain_params_bytes(1 if qk_norm else 0, float(eps), float(rope_base))
     return bytes(_params(qk_norm, eps, rope_base, scaling))
 
 
 def _params(qk_norm, eps, rope_base, scaling=None):
     if scaling is None:                # passed by value: calls share the structure
-        return _plain_params(qk_norm, eps, rope_base)
+        return _plain_params(1 if qk_norm else 0, float(eps), float(rope_base))
     return RopeParams(1 if qk_norm else 0, float(eps), float(rope_base), ROPE_KINDS[scaling.kind],
                       scaling.factor, scaling.original_max_pos, scaling.alpha, scaling.beta)
 
