@@ -386,6 +386,7 @@ constexpr int kBwdWarps = 4;
 constexpr int kBwdResident = 3;                            // CTAs per SM
 constexpr int kBwdMaxCtas = 148 * kBwdResident;
 constexpr int kBwdRing = 4;                                // passes on their way or waiting
+constexpr uint32_t kNoVector = 0x3f803f80u;                // x where there is none: two bf16 ones
 
 struct BackwardArgs {
     const uint16_t *q, *k, *dq_out, *dkc, *dvc;
@@ -402,13 +403,12 @@ struct BackwardArgs {
 };
 
 // One vector: dx of the lane's 16 coordinates in place of dy (ya, yb), and its share of
-// d gain added to dg.  Lanes without a vector (live false) hold zeros and take r = 0: with
-// eps = 0 their r would be infinite and their share of d gain NaN.
+// d gain added to dg.  Lanes without a vector hold dy = 0 and x = 1 (kNoVector): of zeros r
+// would be infinite with eps = 0, and their share of d gain NaN.
 template <int D>
 __device__ __forceinline__ void backward_vector(const uint4 xa, const uint4 xb, uint4 &ya,
                                                 uint4 &yb, const float (&c)[8],
-                                                const float (&s)[8], bool live, bool qk_norm,
-                                                float eps,
+                                                const float (&s)[8], bool qk_norm, float eps,
                                                 const float (&gain)[16], float (&dg)[16]) {
     using S = RopeShape<D>;
     const uint32_t xw[8] = {xa.x, xa.y, xa.z, xa.w, xb.x, xb.y, xb.z, xb.w};
@@ -436,7 +436,7 @@ __device__ __forceinline__ void backward_vector(const uint4 xa, const uint4 xb, 
         }
         const float ss = group_sum<S::kTPV>(ss0 + ss1);
         const float xz = group_sum<S::kTPV>(xz0 + xz1);
-        const float r = live ? rsqrtf(ss * (1.0f / D) + eps) : 0.f;
+        const float r = rsqrtf(ss * (1.0f / D) + eps);
         const float k = -r * (xz * r * (1.0f / D));        // r^3 alone could overflow
 #pragma unroll
         for (int e = 0; e < 16; e += 2) {
@@ -477,6 +477,7 @@ __device__ __forceinline__ void backward_units(const BackwardArgs &A, const Rope
     const int cta = QUERIES ? (int)blockIdx.x : (int)blockIdx.x - A.n_q;
     const unsigned stride = (QUERIES ? A.n_q : gridDim.x - A.n_q) * kBwdWarps;
     const bool norm = A.qk_norm != 0;
+    const uint32_t fill = active ? kNoVector : 0u;         // lanes beyond D/16 add nothing to a norm
 
     float gain[16], dg[16];
     {
@@ -580,7 +581,8 @@ __device__ __forceinline__ void backward_units(const BackwardArgs &A, const Rope
             }
             copy_wait<kBwdRing - 2>();
             const uint4 *place = &sh.ring[warp][stage][0][lane];
-            uint4 ya = make_uint4(0, 0, 0, 0), yb = ya, xa = ya, xb = ya;
+            uint4 ya = make_uint4(0, 0, 0, 0), yb = ya;
+            uint4 xa = make_uint4(fill, fill, fill, fill), xb = xa;
             if (left > 0) {
                 ya = place[0];
                 yb = place[32];
@@ -591,8 +593,7 @@ __device__ __forceinline__ void backward_units(const BackwardArgs &A, const Rope
             }
             load_next(stage == 0 ? kBwdRing - 1 : stage - 1);
             stage = stage == kBwdRing - 1 ? 0 : stage + 1;
-            if (!value)
-                backward_vector<D>(xa, xb, ya, yb, c, s, left > 0, norm, A.eps, gain, dg);
+            if (!value) backward_vector<D>(xa, xb, ya, yb, c, s, norm, A.eps, gain, dg);
             if (left > 0) {
                 *reinterpret_cast<uint4 *>(dst) = ya;
                 *reinterpret_cast<uint4 *>(dst + S::kHalf) = yb;
