@@ -434,7 +434,8 @@ gqa_status kv_cache_read_q4(const void *k_codes, const void *k_scales, const voi
  * m + s c, not rounded to bf16.  Lengths, errors and the workspace's rules as
  * there; gqa_decode_q4_workspace_bytes gives its size (16 bytes are named for calls
  * that merge without it: one chunk, or few and short rows).
- * The chunks' length follows from B, the heads and max_len_host.  Queries and values
+ * The chunks' length follows from B, the heads and max_len_host, and with few rows
+ * from all lens too: equal calls give equal bits.  Queries and values
  * of magnitude up to 2^60 and 2^110 are handled (sums of larger ones can overflow).
  */
 gqa_status gqa_decode_q4(const void *q, const void *k_codes, const void *k_scales,

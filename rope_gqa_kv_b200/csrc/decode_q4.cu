@@ -30,7 +30,8 @@
 // are unpacked; tcgen05 would need them written to shared memory as bf16, four
 // times the bytes that arrived, for 8 columns of work.
 //
-// Work: one CTA per (chunk of the cached slots, KV head x head subgroup, sequence).
+// Work: one CTA per (chunk of the cached slots, KV head x head subgroup, sequence); with
+// few rows the chunks are shared out by the lengths on the device (even_chunk).
 // Its four warps take the chunk's units of kTiles 16-key tiles in turn, each through a ring
 // of its own (asynchronous 16-byte copies; no warp waits for another), with a
 // running softmax: the reference moves, and what is summed is scaled down, only when a
@@ -193,9 +194,35 @@ struct DecQ4Args {
     int32_t *status;
     int max_len, B, Hq, Hkv, Lmax, n_sub, G;               // G: query heads per CTA
     int chunk, n_splits;                                   // slots per CTA, chunks of max_len
+    int places;                                            // or: chunks to share out, see even_chunk
     int cluster;                                           // CTAs of a row's cluster, or 0
     float scale_log2;                  // 2^69 scale / ln 2: the scores come in units of 2^-69
 };
+
+// Calls of few rows share `places` chunks among their sequences by the lengths that these
+// have: the shortest chunk, a multiple of 64 slots, of which the sequences (lane b holds
+// sequence b's length; one that is out of range and lanes without one hold 0) take no more
+// than that, one each at least.  With S slots in all, sum of ceil(len / c) <= S / c + B, so
+// c = S / (places - B) does, and c < S / places does not.
+__device__ __forceinline__ int chunks_of(int len, int chunk, bool mine) {
+    return mine ? max(1, (len + chunk - 1) / chunk) : 0;
+}
+__device__ __forceinline__ int even_chunk(int len, bool mine, int B, int places) {
+    const int S = __reduce_add_sync(0xffffffffu, len);     // B max_len < 2^30
+    int lo = max(1, (S / places + 63) / 64);               // in 64 slots
+    int hi = max(lo, S / (places - B) / 64 + 1);
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (__reduce_add_sync(0xffffffffu, chunks_of(len, 64 * mid, mine)) <= places) hi = mid;
+        else lo = mid + 1;
+    }
+    return 64 * lo;
+}
+// Sequence b's length, 0 where it is out of range.
+__device__ __forceinline__ int len_or_zero(const int32_t *lens, int b, int max_len, int Lmax) {
+    const int len = lens[b];
+    return len < 1 || len > max_len || len > Lmax ? 0 : len;
+}
 
 // Workspace: [(m, l): rows x 2 f32][o: rows x D f32], rows = B x Hq x n_splits, row
 // (b, h, c) = (b * Hq + h) * n_splits + c.
@@ -215,10 +242,24 @@ decode_q4_kernel(const DecQ4Args A) {
     asm volatile("griddepcontrol.launch_dependents;");
     // Chunks in the slowest order: those behind the shorter sequences' ends, which have
     // nothing to do, come last.
-    const int c = blockIdx.z;
-    const int kvh = blockIdx.x / A.n_sub, sub = blockIdx.x - kvh * A.n_sub;
-    const int b = blockIdx.y;
+    int c = blockIdx.z, b = blockIdx.y, chunk = A.chunk;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (!CLUSTER && A.places) {                            // b and c from the lengths
+        const bool mine = lane < A.B;
+        const int mylen = mine ? len_or_zero(A.lens, lane, A.max_len, A.Lmax) : 0;
+        chunk = even_chunk(mylen, mine, A.B, A.places);
+        const int n = chunks_of(mylen, chunk, mine);
+        int end = n;                                       // the first chunk behind the lane's
+#pragma unroll
+        for (int x = 1; x < 32; x <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, end, x);
+            if (lane >= x) end += y;
+        }
+        b = __popc(__ballot_sync(0xffffffffu, end <= c));
+        if (b >= A.B) return;
+        c -= __shfl_sync(0xffffffffu, end - n, b);
+    }
+    const int kvh = blockIdx.x / A.n_sub, sub = blockIdx.x - kvh * A.n_sub;
     const int group = A.Hq / A.Hkv;
     const int h0 = kvh * group + sub * A.G;                // first query head
     const int G = min(A.G, group - sub * A.G);             // query heads of this CTA
@@ -230,7 +271,7 @@ decode_q4_kernel(const DecQ4Args A) {
             for (int i = tid; i < G * D; i += kThreads) A.out[((size_t)b * A.Hq + h0) * D + i] = 0;
         return;
     }
-    const int key0 = c * A.chunk;
+    const int key0 = c * chunk;
     if (key0 >= len) {
         if constexpr (CLUSTER) {                           // (len is the whole cluster's)
             cluster_arrive();
@@ -240,7 +281,7 @@ decode_q4_kernel(const DecQ4Args A) {
         }
         return;
     }
-    const int nk = min(A.chunk, len - key0);
+    const int nk = min(chunk, len - key0);
 
     // ---- the warp's ring ----
     // A lane copies 16 bytes of each 512-byte block of codes, and 16 of each 256 of the
@@ -657,7 +698,7 @@ template <int D, int WPR>
 __global__ void __launch_bounds__(128)
 decode_q4_merge_kernel(const float *__restrict__ ws_ml, const float *__restrict__ ws_o,
                        const int32_t *__restrict__ lens, int max_len, int Hq, int Lmax, int chunk,
-                       int n_splits, int n_rows, uint16_t *__restrict__ out) {
+                       int n_splits, int places, int n_rows, uint16_t *__restrict__ out) {
     __shared__ float sm[4], sl[4];
     __shared__ __align__(16) float so[4][D];
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -673,6 +714,11 @@ decode_q4_merge_kernel(const float *__restrict__ ws_ml, const float *__restrict_
     if (len < 1 || len > max_len || len > Lmax) {          // uniform over the row's warps
         if (live && part == 0) *reinterpret_cast<uint2 *>(o + lane * 4) = make_uint2(0, 0);
         return;
+    }
+    if (places) {
+        const int B = n_rows / Hq;
+        const bool mine = lane < B;
+        chunk = even_chunk(mine ? len_or_zero(lens, lane, max_len, Lmax) : 0, mine, B, places);
     }
     const int ns = (len + chunk - 1) / chunk;
     const float *ml = ws_ml + (size_t)row * n_splits * 2;
@@ -741,7 +787,7 @@ decode_q4_merge_kernel(const float *__restrict__ ws_ml, const float *__restrict_
 
 // How a call is cut: heads per CTA, slots per chunk, chunks of a sequence.
 struct Plan {
-    int G, n_sub, chunk, n_splits, cluster;
+    int G, n_sub, chunk, n_splits, cluster, places;
 };
 
 // Calls without a second kernel ask for so much shared memory that an SM takes two CTAs,
@@ -753,6 +799,7 @@ constexpr int kWideSmem = 100 * 1024;
 constexpr int kClusterPlaces = 148 * 2;
 constexpr int kClusterLen = 4096;      // longer rows want more than eight chunks
 constexpr int kPlaces = 148 * kResident;                   // CTAs resident at once
+constexpr int kShare = 8;              // chunks a sequence, at least, to share out by lengths
 constexpr double kWaves = 8.0 / 3;                         // chunks for each, see make_plan
 
 Plan make_plan(int B, int Hq, int Hkv, int max_len) {
@@ -761,7 +808,7 @@ Plan make_plan(int B, int Hq, int Hkv, int max_len) {
     P.n_sub = (g + kCols - 1) / kCols;
     P.G = (g + P.n_sub - 1) / P.n_sub;
     P.n_sub = (g + P.G - 1) / P.G;
-    P.cluster = 0;
+    P.cluster = P.places = 0;
     // Few, short rows: one to eight chunks of at least 64 slots, merged within a cluster, as
     // long as all CTAs have a place at once (clusters of eight find only half of them: 32 of
     // them took 8.4 us on 4 x 1000 slots of 8 KV heads, of four 5.5) and long chunks fill
@@ -783,6 +830,22 @@ Plan make_plan(int B, int Hq, int Hkv, int max_len) {
     // each place a CTA can have, of at least 64 slots.  64 sequences of 256 .. 2048 slots
     // take 28.7 us at 2.7 of them, 30.2 at 4, 31.2 at 5.3, 29.3 at 1; 4 of 49152 .. 65536
     // 65.6, 65.6, 69.1, 63.5.
+    // Few rows: one chunk for each place a CTA can have, shared out by the lengths on the
+    // device, so that no place is idle when sequences differ or are far from max_len.  24 / 8
+    // heads, D = 128, max_len 65536: 4 sequences of 47179 .. 64169 slots take 57.0 us against
+    // 62.6 with the chunks below, one of 65536 and three of 10 23.9 against 28.6, 4 of 2000
+    // 9.5 against 15.8, 4 of 65536 68.7 against 66.5; 6 of 16384 .. 32768 47.4 against 54.1.
+    // With fewer than kShare chunks a sequence their lengths fit the places badly: 8 of
+    // 18646 .. 25728 take 60.3 against 56.4.  Two chunks for each place: 58.4, 26.1, 10.7, 68.7.
+    const long long share = kPlaces / ((long long)Hkv * P.n_sub);
+    if (B <= 32 && kShare * B <= share && (long long)B * max_len < (1 << 30)) {
+        P.chunk = 64;                                      // the least
+        P.places = (int)share;
+        const int most = (max_len + 63) / 64, left = P.places - B + 1;   // one each to the others
+        P.n_splits = most < left ? most : left;
+        if (P.n_splits > 1) return P;
+        P.places = 0;
+    }
     const long long slots = (long long)B * Hkv * P.n_sub * max_len;
     const long long even = ((long long)((double)slots / (kPlaces * kWaves)) + 63) / 64 * 64;
     const long long most = ((long long)max_len + 63) / 64 * 64;
@@ -803,7 +866,8 @@ cudaError_t launch_split(const DecQ4Args &A, cudaStream_t s) {
     attr[1].val.clusterDim.x = attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = (unsigned)A.cluster;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(A.Hkv * A.n_sub, A.B, CLUSTER ? A.cluster : A.n_splits);
+    cfg.gridDim = A.places ? dim3(A.Hkv * A.n_sub, 1, A.places)
+                           : dim3(A.Hkv * A.n_sub, A.B, CLUSTER ? A.cluster : A.n_splits);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = CLUSTER || A.n_splits == 1 ? kWideSmem : S::kSmem;
     cfg.stream = s;
@@ -838,7 +902,7 @@ cudaError_t launch_decode(const DecQ4Args &A, cudaStream_t s) {
     auto merge = [&](auto kern, int grid) {
         return launch_pdl(kern, dim3((unsigned)grid), 128, s, (const float *)A.ws_ml,
                           (const float *)A.ws_o, A.lens, A.max_len, A.Hq, A.Lmax, A.chunk,
-                          A.n_splits, rows, A.out);
+                          A.n_splits, A.places, rows, A.out);
     };
     return A.n_splits > 32 ? merge(decode_q4_merge_kernel<D, 4>, rows)
                            : merge(decode_q4_merge_kernel<D, 1>, (rows + 3) / 4);
@@ -1023,6 +1087,7 @@ extern "C" gqa_status gqa_decode_q4(const void *q, const void *k_codes, const vo
     A.n_splits = P.n_splits;
     A.chunk = P.chunk;
     A.cluster = P.cluster;
+    A.places = P.places;
     A.n_sub = P.n_sub;
     A.G = P.G;
     A.scale_log2 = (scale > 0.f ? scale : 1.0f / sqrtf((float)D)) * 1.4426950408889634f * 0x1p69f;

@@ -300,6 +300,52 @@ def test_decode_bad_lengths_give_zeros(cuda_lib, max_len):
     assert ((out[3:4].cpu().double() - want).abs() <= tol).all()
 
 
+@pytest.mark.parametrize("D,Hq,Hkv,max_len,lens", [
+    (128, 6, 2, 8960, [8960, 1, 64, 65]), (64, 3, 1, 12000, [12000] * 3),
+    (96, 4, 4, 5000, [4097, 5000, 1, 1, 129, 128]), (128, 24, 8, 4224, [4224, 10, 10, 10, 10, 10]),
+    (64, 1, 1, 4500, [1 + 145 * i for i in range(32)]), (128, 9, 1, 30000, [1]),
+    (128, 2, 1, 30000, [64, 63]), (96, 5, 1, 6000, [4608] * 27)])
+def test_decode_few_rows_share_the_chunks_by_length(cuda_lib, D, Hq, Hkv, max_len, lens):
+    """Long capacities with few rows: the cut follows the lengths, on the device."""
+    B, L = len(lens), (max_len + 127) // 128 * 128
+    q = torch.randn(B, Hq, D, generator=torch.Generator().manual_seed(max_len)).to(BF)
+    _check_decode(q, _random_cache(D + B, B, Hkv, L, D), torch.tensor(lens), max_len, str(lens[:4]))
+
+
+def test_decode_few_rows_with_bad_lengths_and_replayed_with_others(cuda_lib):
+    B, Hq, Hkv, D, L, max_len = 5, 6, 2, 64, 9088, 9000
+    parts = _random_cache(77, B, Hkv, L, D)
+    cache = _on_gpu(parts)
+    q = torch.randn(B, Hq, D, generator=torch.Generator().manual_seed(7)).to(BF)
+    qd, status = q.to(DEV), torch.zeros(1, dtype=torch.int32, device=DEV)
+    lens = torch.tensor([5000, 0, 9001, 700, -3], dtype=torch.int32, device=DEV)
+    ws = gqa.decode_q4_workspace(B, Hq, Hkv, D, max_len, DEV)
+    ws.view(torch.float32).fill_(math.nan)
+    out = torch.full((B, Hq, D), 7.0, dtype=BF, device=DEV)
+    run = lambda: gqa.gqa_decode_q4(qd, cache, lens, max_len, out=out, workspace=ws, status=status)
+    run()
+    torch.cuda.synchronize()
+    assert status.item() == gqa.GQA_DEV_BAD_LEN | gqa.GQA_DEV_CAPACITY
+    good = [0, 3]
+    want, tol = ref.decode(q[good], [t[good] for t in parts], torch.tensor([5000, 700]), None)
+    assert ((out[good].cpu().double() - want).abs() <= tol).all()
+    assert (out[[1, 2, 4]] == 0).all()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for n in ([1, 2, 3, 4, 5], [9000, 1, 1, 1, 1], [9000] * 5, [3000, 4000, 64, 65, 8999]):
+        lens.copy_(torch.tensor(n, dtype=torch.int32))
+        status.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert status.item() == 0
+        replayed = out.clone()
+        run()
+        assert torch.equal(out, replayed)
+        want, tol = ref.decode(q, parts, torch.tensor(n), None)
+        assert ((replayed.cpu().double() - want).abs() <= tol).all(), n
+
+
 def test_offsets_beyond_32_bits(cuda_lib):
     """A cache of more than 2^31 bytes of codes: the last sequence's newest slots are
     written, read back and attended to.  Every other slot is zero (score 0, value 0), so
@@ -332,8 +378,9 @@ def test_offsets_beyond_32_bits(cuda_lib):
     w = torch.exp(s - top)
     want = torch.einsum("bhs,bhsd->bhd", w, vals[1]) / (w.sum(-1, keepdim=True) +
                                                           (L - 3) * torch.exp(-top))
-    # 3 live keys against 2 million: the weights' sum is off by at most a few hundred
-    # fp32 units (8194 chunks in groups of 32), scores of up to ~60 by 1e-4
+    # 3 live keys against 2 million: a lane adds a 64th of a chunk's weights (some 1300 of
+    # 2^21 / 26 slots) one after the other, which is off by at most as many fp32 units,
+    # 1e-4 of the sum; scores of up to ~60 are off by 1e-4
     assert ((out.cpu().double() - want).abs() <= (2.0 ** -8 + 5e-4) * want.abs() + 1e-6).all()
     k3 = v3 = cache = None
 

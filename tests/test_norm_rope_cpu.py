@@ -178,6 +178,9 @@ def test_workspace_sizes(lib):
     # whatever the cut: one to max_len / 64 rows of D + 2 floats per query head
     row = 64 * 24 * 130 * 4
     assert 2 * row <= f(64, 24, 8, 128, 2049) <= 33 * row + 16
+    # few rows: a chunk for each place, but one for each of the other sequences
+    assert f(4, 24, 8, 128, 65536) == 4 * 24 * (148 * 3 // 8 - 3) * 130 * 4
+    assert f(1, 1, 1, 64, 4160) == 65 * 66 * 4 + 8          # (m, l) up to a 16-byte boundary
 
 
 # ---------------------------------------------------------------------------
