@@ -825,6 +825,22 @@ Plan make_plan(int B, int Hq, int Hkv, int max_len) {
         if (P.chunk <= 1024 || 8 * c * rows >= 7 * kClusterPlaces) return P;
         P.cluster = 0;
     }
+    // Few rows: one chunk for each place a CTA can have, shared out by the lengths on the
+    // device, so that no place is idle when sequences differ or are far from max_len.  24 / 8
+    // heads, D = 128, max_len 65536: 4 sequences of 47179 .. 64169 slots take 57.0 us against
+    // 62.6 with the chunks below, one of 65536 and three of 10 23.9 against 28.6, 4 of 2000
+    // 9.5 against 15.8, 4 of 65536 68.7 against 66.5; 6 of 16384 .. 32768 47.4 against 54.1.
+    // With fewer than kShare chunks a sequence their lengths fit the places badly: 8 of
+    // 18646 .. 25728 take 60.3 against 56.4.  Two chunks for each place: 58.4, 26.1, 10.7, 68.7.
+    const long long share = kPlaces / ((long long)Hkv * P.n_sub);
+    if (B <= 32 && kShare * B <= share && (long long)B * max_len < (1 << 30)) {
+        P.chunk = 64;                                      // the least
+        P.places = (int)share;
+        const int most = (max_len + 63) / 64, left = P.places - B + 1;   // one each to the others
+        P.n_splits = most < left ? most : left;
+        if (P.n_splits > 1) return P;
+        P.places = 0;
+    }
     // Longer chunks leave less to start up and merge, shorter ones spread a call evenly
     // over the SMs (sequences shorter than max_len leave theirs out): kWaves chunks for
     // each place a CTA can have, of at least 64 slots.  64 sequences of 256 .. 2048 slots
