@@ -432,8 +432,8 @@ gqa_status kv_cache_read_q4(const void *k_codes, const void *k_scales, const voi
 /*
  * gqa_decode_q4 -- gqa_decode against a 4-bit cache; K and V are the values
  * m + s c, not rounded to bf16.  Lengths, errors and the workspace's rules as
- * there; gqa_decode_q4_workspace_bytes gives its size (16 bytes are named for calls
- * that merge without it: one chunk, or few and short rows).
+ * there; gqa_decode_q4_workspace_bytes gives its size, which serves every shorter
+ * max_len_host too (16 bytes where all of these merge without it).
  * The chunks' length follows from B, the heads and max_len_host, and with few rows
  * from all lens too: equal calls give equal bits.  Queries and values
  * of magnitude up to 2^60 and 2^110 are handled (sums of larger ones can overflow).
@@ -444,7 +444,8 @@ gqa_status gqa_decode_q4(const void *q, const void *k_codes, const void *k_scale
                          float scale, void *ws, size_t ws_bytes, int32_t *status_dev,
                          void *stream);
 
-/* Bytes of workspace gqa_decode_q4 needs for these sizes (0 on invalid sizes). */
+/* Bytes of workspace gqa_decode_q4 needs for these sizes and any shorter max_len (0 on
+ * invalid sizes). */
 size_t gqa_decode_q4_workspace_bytes(int B, int Hq, int Hkv, int D, int max_len);
 
 /*

@@ -43,6 +43,7 @@
 // thread-block cluster, each hands its (m, l, o) to the first one's shared memory, and
 // that one writes the output.
 #include <atomic>
+#include <cmath>
 #include <type_traits>
 
 #include "q4.cuh"
@@ -788,6 +789,7 @@ decode_q4_merge_kernel(const float *__restrict__ ws_ml, const float *__restrict_
 // How a call is cut: heads per CTA, slots per chunk, chunks of a sequence.
 struct Plan {
     int G, n_sub, chunk, n_splits, cluster, places;
+    int most_splits;                   // n_splits of any shorter max_len, at most
 };
 
 // Calls without a second kernel ask for so much shared memory that an SM takes two CTAs,
@@ -822,6 +824,7 @@ Plan make_plan(int B, int Hq, int Hkv, int max_len) {
         P.chunk = ((max_len + c - 1) / c + 63) / 64 * 64;
         P.n_splits = (max_len + P.chunk - 1) / P.chunk;
         P.cluster = c > 1 ? c : 0;                         // one chunk needs none
+        P.most_splits = 1;             // (shorter calls merge this way too: nothing in memory)
         if (P.chunk <= 1024 || 8 * c * rows >= 7 * kClusterPlaces) return P;
         P.cluster = 0;
     }
@@ -833,25 +836,39 @@ Plan make_plan(int B, int Hq, int Hkv, int max_len) {
     // With fewer than kShare chunks a sequence their lengths fit the places badly: 8 of
     // 18646 .. 25728 take 60.3 against 56.4.  Two chunks for each place: 58.4, 26.1, 10.7, 68.7.
     const long long share = kPlaces / ((long long)Hkv * P.n_sub);
-    if (B <= 32 && kShare * B <= share && (long long)B * max_len < (1 << 30)) {
-        P.chunk = 64;                                      // the least
-        P.places = (int)share;
-        const int most = (max_len + 63) / 64, left = P.places - B + 1;   // one each to the others
-        P.n_splits = most < left ? most : left;
-        if (P.n_splits > 1) return P;
-        P.places = 0;
+    const int most = (int)((max_len + 63LL) / 64);         // chunks of a sequence
+    // The chunks below have at least floor(slots / places) slots, and 64: a sequence has
+    // no more of them than this, at any length.
+    const double even_most = std::ceil(kPlaces * kWaves / (double)rows * (65.0 / 64));
+    P.most_splits = even_most < most ? (int)even_most : most;
+    if (B <= 32 && kShare * B <= share) {
+        const int left = (int)share - B + 1;               // one each to the others
+        const int n = most < left ? most : left;
+        P.most_splits = n > P.most_splits ? n : P.most_splits;
+        if (n > 1 && (long long)B * max_len < (1 << 30)) {
+            P.chunk = 64;                                  // the least
+            P.places = (int)share;
+            P.n_splits = n;
+            return P;
+        }
     }
     // Longer chunks leave less to start up and merge, shorter ones spread a call evenly
     // over the SMs (sequences shorter than max_len leave theirs out): kWaves chunks for
     // each place a CTA can have, of at least 64 slots.  64 sequences of 256 .. 2048 slots
     // take 28.7 us at 2.7 of them, 30.2 at 4, 31.2 at 5.3, 29.3 at 1; 8 of 18646 .. 32768
     // 53.0, 58.0, 58.1, 62.5.
-    const long long slots = (long long)B * Hkv * P.n_sub * max_len;
+    const long long slots = rows * max_len;
     const long long even = ((long long)((double)slots / (kPlaces * kWaves)) + 63) / 64 * 64;
-    const long long most = ((long long)max_len + 63) / 64 * 64;
-    P.chunk = (int)(even < 64 ? 64 : even > most ? most : even);
+    P.chunk = (int)(even < 64 ? 64 : even > 64LL * most ? 64LL * most : even);
     P.n_splits = (max_len + P.chunk - 1) / P.chunk;
     return P;
+}
+
+// Partials of that many chunks a row; the outputs start on a 16-byte boundary.
+size_t workspace_bytes(int B, int Hq, int D, int n_splits) {
+    if (n_splits == 1) return 16;                          // no second kernel: not used
+    const size_t rows = (size_t)B * Hq * n_splits;
+    return (rows * 2 * 4 + 15) / 16 * 16 + rows * (size_t)D * 4;
 }
 
 template <int D, bool CLUSTER>
@@ -1040,11 +1057,7 @@ extern "C" gqa_status kv_cache_read_q4(const void *k_codes, const void *k_scales
 extern "C" size_t gqa_decode_q4_workspace_bytes(int B, int Hq, int Hkv, int D, int max_len) {
     if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || max_len < 1 || !gqa_host::head_dim_ok(D))
         return 0;
-    const gqa::Plan P = gqa::make_plan(B, Hq, Hkv, max_len);
-    if (P.n_splits == 1 || P.cluster) return 16;           // no second kernel: not used
-    const size_t rows = (size_t)B * Hq * P.n_splits;
-    // The partial outputs start on a 16-byte boundary.
-    return (rows * 2 * 4 + 15) / 16 * 16 + rows * (size_t)D * 4;
+    return gqa::workspace_bytes(B, Hq, D, gqa::make_plan(B, Hq, Hkv, max_len).most_splits);
 }
 
 extern "C" gqa_status gqa_decode_q4(const void *q, const void *k_codes, const void *k_scales,
@@ -1064,9 +1077,10 @@ extern "C" gqa_status gqa_decode_q4(const void *q, const void *k_codes, const vo
     if (Lmax % 128 != 0) return GQA_ERR_INVALID_ARG;
     if (max_len_host < 1) return GQA_ERR_INVALID_ARG;
     if (max_len_host > Lmax) return GQA_ERR_CAPACITY;
-    const size_t need = gqa_decode_q4_workspace_bytes(B, Hq, Hkv, D, max_len_host);
     const gqa::Plan P = gqa::make_plan(B, Hq, Hkv, max_len_host);
-    if (!ws || ws_bytes < need || !aligned16(ws)) return GQA_ERR_WORKSPACE;
+    if (!ws || !aligned16(ws) ||
+        ws_bytes < gqa::workspace_bytes(B, Hq, D, P.cluster ? 1 : P.n_splits))
+        return GQA_ERR_WORKSPACE;
     gqa::DecQ4Args A = {};
     A.q = static_cast<const uint16_t *>(q);
     A.kc = static_cast<const uint8_t *>(k_codes);

@@ -183,6 +183,16 @@ def test_workspace_sizes(lib):
     assert f(1, 1, 1, 64, 4160) == 65 * 66 * 4 + 8          # (m, l) up to a 16-byte boundary
 
 
+@pytest.mark.parametrize("B,Hq,Hkv", [(1, 1, 1), (1, 8, 8), (4, 24, 8), (6, 24, 8), (8, 24, 8),
+                                      (16, 16, 2), (33, 8, 8), (64, 24, 8), (100, 4, 1),
+                                      (125, 8, 8), (600, 32, 4)])
+def test_a_workspace_of_the_capacity_serves_every_shorter_call(lib, B, Hq, Hkv):
+    """Allocated once for the longest call, used for all: the size never falls with max_len."""
+    f = lambda n: lib.gqa_decode_q4_workspace_bytes(B, Hq, Hkv, 128, n)
+    sizes = [f(n) for n in list(range(1, 6000)) + list(range(6000, 140000, 61))]
+    assert sizes == sorted(sizes)
+
+
 # ---------------------------------------------------------------------------
 # refusals of the binding (host tensors; device ones are refused in the GPU tests)
 # ---------------------------------------------------------------------------
