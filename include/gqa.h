@@ -349,7 +349,7 @@ typedef struct {
  *   max_pos0_host: host-known upper bound of pos0 (-1: none).  Without n_tok,
  *     max_pos0_host + T > Lmax is GQA_ERR_CAPACITY.
  *   new_len: optional device int32 [B] output, pos0[b] + n_tok[b] (pos0[b] where
- *     n_tok[b] is out of range).  It must not overlap pos0 or n_tok.
+ *     n_tok[b] is out of range).  It must not overlap pos0, n_tok or x->pos.
  */
 gqa_status gqa_norm_rope_append(const void *q, const void *k, const void *v, void *q_out,
                                 void *k_cache, void *v_cache, const int32_t *pos0,

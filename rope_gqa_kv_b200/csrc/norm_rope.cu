@@ -767,13 +767,18 @@ gqa_status check_append(const void *q, const void *k, const void *v, const void 
     if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) ||
         !aligned4(pos0) || !aligned4(n_tok) || !aligned4(new_len))
         return GQA_ERR_INVALID_ARG;
-    auto overlaps = [&](const int32_t *a) { return a && new_len < a + B && a < new_len + B; };
-    if (new_len && (overlaps(pos0) || overlaps(n_tok))) return GQA_ERR_INVALID_ARG;
     if (!params_ok(p)) return GQA_ERR_INVALID_ARG;
     if (!head_dim_ok(D)) return GQA_ERR_UNSUPPORTED;
     if (!inputs_ok(x, p, D)) return GQA_ERR_INVALID_ARG;
     if (Lmax % 128 != 0) return GQA_ERR_INVALID_ARG;
     if ((long long)B * T > 0x7fffffffLL) return GQA_ERR_INVALID_ARG;
+    // A CTA writes new_len while others still read these, with no order between them.
+    auto overlaps = [&](const int32_t *a, long long n) {
+        return a && new_len < a + n && a < new_len + B;
+    };
+    if (new_len && (overlaps(pos0, B) || overlaps(n_tok, B) ||
+                    (x && overlaps(x->pos, (long long)x->n_axes * B * T))))
+        return GQA_ERR_INVALID_ARG;
     if ((long long)(q ? Hq : 0) + 2LL * Hkv > 0x3fffffffLL) return GQA_ERR_INVALID_ARG;
     if (T > Lmax && !n_tok) return GQA_ERR_CAPACITY;
     if (max_pos0_host >= 0 && !n_tok && (long long)max_pos0_host + T > Lmax)

@@ -248,3 +248,13 @@ def test_parameters_follow_a_value_that_changes_in_place():
     eps.fill_(0.5)
     assert _lib._params_bytes(True, eps, 1e4, None) != first
     assert _lib._params(True, eps, 1e4).eps == 0.5
+
+
+@pytest.mark.parametrize("over", [
+    dict(T=1, x=_inputs(pos=0x10000)), dict(T=1, B=2, x=_inputs(pos=0x10004)),
+    dict(T=1, B=2, x=_inputs(pos=0x10000 - 4)), dict(x=_inputs(pos=0x10000 - 60)),
+    dict(T=1, B=4, x=_inputs(pos=0x10000 - 44, n_axes=3, pair_axis=[0, 1, 2]))])
+def test_append_refuses_new_lengths_written_over_positions(lib, over):
+    """new_len (B words at F) is written while other warps still read pos (n_axes B T)."""
+    assert lib.gqa_norm_rope_append(*_append_args(False, **dict(over, new_len=F))) == 1
+    assert lib.gqa_norm_rope_append_q4(*_append_args(True, **dict(over, new_len=F))) == 1
