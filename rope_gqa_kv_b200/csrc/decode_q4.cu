@@ -35,7 +35,10 @@
 // Its four warps take the chunk's units of kTiles 16-key tiles in turn, each through a ring
 // of its own (asynchronous 16-byte copies; no warp waits for another), with a
 // running softmax: the reference moves, and what is summed is scaled down, only when a
-// score passes it by more than 8, i.e. hardly ever after the first tile.  At the end
+// score passes it by more than 8, i.e. hardly ever after the first tile.  References and
+// the chunks' m are scores before scaling: the largest is then exactly 0 from itself, while
+// against a rounded product it would be off by 2^-24 of the score, more than an exponent's
+// range for scores from 2^31 on.  At the end
 // the warps' statistics and partial outputs are merged in shared memory, the chunk's
 // (m, l, o) goes to the workspace and a second kernel, a programmatic dependent,
 // merges the chunks.  When one chunk covers max_len the CTA writes the output itself.
@@ -60,8 +63,8 @@ constexpr int kTiles = 2;              // tiles of 16 keys that a warp takes at 
 constexpr int kStages = 3;             // such units in a warp's ring
 constexpr int kCols = 8;               // columns of the mma: query heads of a CTA, at most
 constexpr int kMaxCluster = 8;         // CTAs of a cluster
-constexpr float kSlack = 8.0f;         // a score may pass the softmax reference by this
-constexpr float kNoRef = -1e30f;       // the reference before any score: finite, so that
+constexpr float kSlack = 8.0f;         // a score may pass the softmax reference by this (log2)
+constexpr float kNoRef = -3.402823466e38f;   // before any score: the lowest finite value, so that
                                        // 2^(a score of -inf - it) is 0
 
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -198,6 +201,7 @@ struct DecQ4Args {
     int places;                                            // or: chunks to share out, see even_chunk
     int cluster;                                           // CTAs of a row's cluster, or 0
     float scale_log2;                  // 2^69 scale / ln 2: the scores come in units of 2^-69
+    float slack;                       // kSlack in the scores' units
 };
 
 // Calls of few rows share `places` chunks among their sequences by the lengths that these
@@ -480,9 +484,7 @@ decode_q4_kernel(const DecQ4Args A) {
             n0 = fmaxf(n0, fmaxf(sc[j][0], sc[j][2]));
             n1 = fmaxf(n1, fmaxf(sc[j][1], sc[j][3]));
         }
-        n0 *= A.scale_log2;
-        n1 *= A.scale_log2;
-        if (__any_sync(0xffffffffu, fmaxf(n0 - ref[0], n1 - ref[1]) > kSlack ||
+        if (__any_sync(0xffffffffu, fmaxf(n0 - ref[0], n1 - ref[1]) > A.slack ||
                                         bf16lo(smax) >= cap)) {
 #pragma unroll
             for (int x = 4; x < 32; x <<= 1) {
@@ -495,7 +497,8 @@ decode_q4_kernel(const DecQ4Args A) {
             const uint32_t neb = max(eb, min(max((smax >> 7) & 0xffu, 17u), 235u));
             // 2^(eb - neb), 0 at the first unit (where all sums are zero) and below 2^-126
             const float es = neb - eb > 126u ? 0.f : __uint_as_float((127u - (neb - eb)) << 23);
-            const float f0 = ex2(ref[0] - n0), f1 = ex2(ref[1] - n1);
+            const float f0 = ex2((ref[0] - n0) * A.scale_log2);
+            const float f1 = ex2((ref[1] - n1) * A.scale_log2);
             l[0] *= f0;
             l[1] *= f1;
             eb = neb;
@@ -524,7 +527,7 @@ decode_q4_kernel(const DecQ4Args A) {
 #pragma unroll
         for (int j = 0; j < U; ++j) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) sc[j][e] = ex2(fmaf(sc[j][e], A.scale_log2, -ref[e & 1]));
+            for (int e = 0; e < 4; ++e) sc[j][e] = ex2((sc[j][e] - ref[e & 1]) * A.scale_log2);
             l[0] += sc[j][0] + sc[j][2];
             l[1] += sc[j][1] + sc[j][3];
             uint32_t wa[NG], wb[NG], wc[NG], wd[NG];       // rows 2 kk, 2 kk + 1, and 8 on
@@ -608,7 +611,7 @@ decode_q4_kernel(const DecQ4Args A) {
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
             const float m = wml[(w * kCols + tid) * 2];
-            const float f = ex2(m - M);                    // 0 for a warp without a tile
+            const float f = ex2((m - M) * A.scale_log2);   // 0 for a warp without a tile
             sw[w * kCols + tid] = f;
             L = fmaf(f, wml[(w * kCols + tid) * 2 + 1], L);
         }
@@ -678,7 +681,7 @@ decode_q4_kernel(const DecQ4Args A) {
             for (int i = 1; i < n; ++i) M = fmaxf(M, ml[i * kFloats]);
             float L = 0.f, a0 = 0.f, a1 = 0.f;
             for (int i = 0; i < n; ++i) {
-                const float f = ex2(ml[i * kFloats] - M);
+                const float f = ex2((ml[i * kFloats] - M) * A.scale_log2);
                 const float2 v = *reinterpret_cast<const float2 *>(got + i * kFloats + h * D + d);
                 L = fmaf(f, ml[i * kFloats + 1], L);
                 a0 = fmaf(f, v.x, a0);
@@ -699,7 +702,8 @@ template <int D, int WPR>
 __global__ void __launch_bounds__(128)
 decode_q4_merge_kernel(const float *__restrict__ ws_ml, const float *__restrict__ ws_o,
                        const int32_t *__restrict__ lens, int max_len, int Hq, int Lmax, int chunk,
-                       int n_splits, int places, int n_rows, uint16_t *__restrict__ out) {
+                       int n_splits, int places, int n_rows, float scale_log2,
+                       uint16_t *__restrict__ out) {
     __shared__ float sm[4], sl[4];
     __shared__ __align__(16) float so[4][D];
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -737,8 +741,8 @@ decode_q4_merge_kernel(const float *__restrict__ ws_ml, const float *__restrict_
         const float2 mi = lane < n ? *reinterpret_cast<const float2 *>(ml + 2 * (base + lane))
                                    : make_float2(-INFINITY, 0.f);
         const float mn = fmaxf(M, warp_max(mi.x));
-        const float alpha = M == -INFINITY ? 0.f : ex2(M - mn);
-        const float w = lane < n ? ex2(mi.x - mn) : 0.f;
+        const float alpha = M == -INFINITY ? 0.f : ex2((M - mn) * scale_log2);
+        const float w = lane < n ? ex2((mi.x - mn) * scale_log2) : 0.f;
         L = fmaf(L, alpha, warp_sum(w * mi.y));
         a0 *= alpha;
         a1 *= alpha;
@@ -768,7 +772,7 @@ decode_q4_merge_kernel(const float *__restrict__ ws_ml, const float *__restrict_
         L = a0 = a1 = a2 = a3 = 0.f;
 #pragma unroll
         for (int w = 0; w < WPR; ++w) {
-            const float f = sm[w] == -INFINITY ? 0.f : ex2(sm[w] - top);
+            const float f = sm[w] == -INFINITY ? 0.f : ex2((sm[w] - top) * scale_log2);
             L = fmaf(f, sl[w], L);
             if (live) {
                 const float4 v = *reinterpret_cast<const float4 *>(&so[w][lane * 4]);
@@ -919,7 +923,7 @@ cudaError_t launch_decode(const DecQ4Args &A, cudaStream_t s) {
     auto merge = [&](auto kern, int grid) {
         return launch_pdl(kern, dim3((unsigned)grid), 128, s, (const float *)A.ws_ml,
                           (const float *)A.ws_o, A.lens, A.max_len, A.Hq, A.Lmax, A.chunk,
-                          A.n_splits, A.places, rows, A.out);
+                          A.n_splits, A.places, rows, A.scale_log2, A.out);
     };
     return A.n_splits > 32 ? merge(decode_q4_merge_kernel<D, 4>, rows)
                            : merge(decode_q4_merge_kernel<D, 1>, (rows + 3) / 4);
@@ -1105,6 +1109,7 @@ extern "C" gqa_status gqa_decode_q4(const void *q, const void *k_codes, const vo
     A.n_sub = P.n_sub;
     A.G = P.G;
     A.scale_log2 = (scale > 0.f ? scale : 1.0f / sqrtf((float)D)) * 1.4426950408889634f * 0x1p69f;
+    A.slack = gqa::kSlack / A.scale_log2;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const cudaError_t e = D == 64   ? gqa::launch_decode<64>(A, s)
                           : D == 96 ? gqa::launch_decode<96>(A, s)

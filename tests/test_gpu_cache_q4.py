@@ -587,3 +587,42 @@ def test_the_checks_in_python_lead_to_the_same_calls(cuda_lib, monkeypatch):
     slower = run(side)
     for got in (fast, slow, slower):
         assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+@pytest.mark.parametrize("eq,ek", [(12, 0), (28, 0), (31, 0), (40, 0), (60, 0), (60, 50)])
+@pytest.mark.parametrize("D,n", [(64, 100), (96, 700), (128, 4500)])
+def test_decode_scores_of_any_size(cuda_lib, eq, ek, D, n):
+    """Scores of up to +-2^118, exact in fp32, all of one sign: q has one coordinate, +-2^eq,
+    and K's rows are constants 2^ek times 141 .. 239 with one 255 (which takes all of the
+    heads with a positive q) and one 128 (the others': their scores are all negative)."""
+    B, Hq, Hkv, L = 2, 4, 2, (n + 127) // 128 * 128
+    g = torch.Generator().manual_seed(n + eq)
+    parts = _random_cache(n, B, Hkv, L, D)
+    lens = torch.tensor([n, n // 2 + 1])
+    m = torch.randint(141, 240, (B, Hkv, L), generator=g).double()
+    best = torch.empty(B, Hkv, 2, dtype=torch.long)
+    for b in range(B):
+        for h in range(Hkv):
+            at = torch.randperm(int(lens[b]), generator=g)[:2]
+            m[b, h, at[0]], m[b, h, at[1]] = 255, 128
+            best[b, h] = at
+    parts[1] = torch.stack((torch.zeros(B, Hkv, L, D // 32, dtype=torch.float64),
+                            (m * 2.0 ** ek).unsqueeze(-1).expand(B, Hkv, L, D // 32)), -1).to(BF)
+    q = torch.zeros(B, Hq, D, dtype=BF)
+    q[:, 0::2, 3], q[:, 1::2, 3] = 2.0 ** eq, -2.0 ** eq
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    out = gqa.gqa_decode_q4(q.to(DEV), _on_gpu(parts), lens.to(torch.int32).to(DEV), n,
+                            status=status).cpu().double()
+    assert status.item() == 0
+    # the other weights are below exp(-13 * 2^12 / sqrt(128)) = 0 and the best one's is exactly 1:
+    # what is left is p s to fp16, the last sums (as in norm_rope_reference.decode) and bf16
+    grp = (torch.arange(D) % (D // 2)) // 16
+    vals = ref.values(parts[2], parts[3])
+    step, low = parts[3].double()[..., 0][..., grp], parts[3].double()[..., 1][..., grp]
+    for b in range(B):
+        for h in range(Hq):
+            at = (b, h // 2, int(best[b, h // 2, h % 2]))
+            want = vals[at]
+            tol = 2.0 ** -8 * want.abs() + 1.01 * (2.0 ** -11 * 15 * step[at] + 80 * ref.U32 *
+                                                   (15 * step[at] + low[at].abs()))
+            assert ((out[b, h] - want).abs() <= tol).all(), (b, h)
