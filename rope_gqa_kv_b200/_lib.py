@@ -11,6 +11,8 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+import types
+import warnings
 
 import torch
 
@@ -180,20 +182,31 @@ def load(path: str | None = None):
             fn = getattr(lib, name)
             fn.restype = res
             fn.argtypes = args
-        try:
-            from . import _fastargs
-        except ImportError as e:
-            raise RuntimeError("the binding's argument checks (_fastargs.so) are not built; "
-                               "build them with `python -m rope_gqa_kv_b200.build`") from e
+        fast = _native_checks(lib)
+        _fast, _fast_pointers = fast, fast.pointers
+        _lib = lib
+    return _lib
+
+
+def _native_checks(lib):
+    """csrc/fastargs.c, or, where it is not built or this torch lacks the interface it
+    reads tensors through, functions that leave every call to the checks in Python."""
+    try:
+        from . import _fastargs
         _fastargs.setup(torch.Tensor.__dlpack_c_exchange_api__, (
             (torch.bfloat16, 4, 16), (torch.int32, 0, 32), (torch.uint8, 1, 8),
             (torch.float32, 2, 32)))
         _fastargs.entries(tuple(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
             "gqa_norm_rope_append", "gqa_norm_rope_append_q4", "gqa_norm_rope_append_backward",
             "kv_cache_read_q4", "gqa_decode_q4")))
-        _fast, _fast_pointers = _fastargs, _fastargs.pointers
-        _lib = lib
-    return _lib
+        return _fastargs
+    except (ImportError, AttributeError, RuntimeError, TypeError, ValueError) as e:
+        warnings.warn("arguments are checked in Python, some 10 us a call slower: %s" % e,
+                      RuntimeWarning, stacklevel=3)
+        def none(*args):
+            return None
+        return types.SimpleNamespace(append=none, backward=none, read_back=none, decode=none,
+                                     cache=none, pointers=none)
 
 
 def status_string(status: int) -> str:

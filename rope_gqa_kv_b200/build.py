@@ -6,7 +6,8 @@ Each .cu is compiled to an object in _build/ (parallel), then linked into
 rope_gqa_kv_b200/libgqa.so with the CUDA runtime linked statically.  A source
 is rebuilt when it, or any header it may include, is newer than its object.
 csrc/fastargs.c, the argument checks of the Python binding, becomes the extension
-module rope_gqa_kv_b200/_fastargs.so (gcc).
+module rope_gqa_kv_b200/_fastargs.so (gcc), for one Python and one torch; where it does
+not compile the binding checks in Python.
 """
 from __future__ import annotations
 
@@ -18,6 +19,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -26,6 +28,7 @@ OBJ_DIR = os.path.join(ROOT, "_build", "gqa")
 LIB = os.path.join(PKG, "libgqa.so")
 ARGS_SRC = os.path.join(CSRC, "fastargs.c")
 ARGS_LIB = os.path.join(PKG, "_fastargs.so")
+ARGS_FOR = os.path.join(OBJ_DIR, "fastargs.txt")          # what it was built for
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
@@ -58,18 +61,30 @@ def _compile(src: str, verbose: bool) -> tuple[str, str]:
 
 
 def _build_args(force: bool) -> None:
-    if not force and os.path.exists(ARGS_LIB) and \
-            os.path.getmtime(ARGS_LIB) >= max(os.path.getmtime(f) for f in [ARGS_SRC] + _headers()):
-        return
     import torch
+    made_for = "python %s, torch %s\n" % (sys.version, torch.__version__)
+    if not force and os.path.exists(ARGS_LIB) and os.path.exists(ARGS_FOR) and \
+            open(ARGS_FOR).read() == made_for and os.path.getmtime(ARGS_LIB) >= max(
+                os.path.getmtime(f) for f in [ARGS_SRC] + _headers()):
+        return
     tmp = ARGS_LIB + ".tmp%d" % os.getpid()
     cmd = [shutil.which("gcc") or "gcc", "-O2", "-Wall", "-shared", "-fPIC",
            "-I", sysconfig.get_paths()["include"], "-I", os.path.join(ROOT, "include"),
            "-I", os.path.join(os.path.dirname(torch.__file__), "include"), ARGS_SRC, "-o", tmp]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError("gcc failed:\n%s\n%s" % (" ".join(cmd), r.stderr))
+    try:
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        err = r.stderr if r.returncode else None
+    except OSError as e:
+        err = str(e)
+    if err is not None:                # the library works without it, but not with an old one
+        if os.path.exists(ARGS_LIB):
+            os.remove(ARGS_LIB)
+        warnings.warn("gcc failed, arguments will be checked in Python:\n%s\n%s" %
+                      (" ".join(cmd), err), RuntimeWarning)
+        return
     os.replace(tmp, ARGS_LIB)
+    with open(ARGS_FOR, "w") as f:
+        f.write(made_for)
 
 
 def build(force: bool = False, verbose: bool = False, jobs: int = 0) -> str:

@@ -19,7 +19,8 @@
  *       tensors of a device that is not the current one).
  *
  * After a None the caller looks at the arguments one by one, to say which one does not
- * fit (or to accept what only that path can): nothing is refused here alone.
+ * fit (or to accept what only that path can): nothing is refused here alone, and without
+ * this module (a torch without that table) the caller takes that path for every call.
  */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>

@@ -2,6 +2,7 @@
 the GPU tests compare with, and every refusal of the C entries and of the binding."""
 import ctypes
 import math
+import sys
 
 import pytest
 import torch
@@ -258,3 +259,71 @@ def test_append_refuses_new_lengths_written_over_positions(lib, over):
     """new_len (B words at F) is written while other warps still read pos (n_axes B T)."""
     assert lib.gqa_norm_rope_append(*_append_args(False, **dict(over, new_len=F))) == 1
     assert lib.gqa_norm_rope_append_q4(*_append_args(True, **dict(over, new_len=F))) == 1
+
+
+# ---------------------------------------------------------------------------
+# without the native argument checks
+# ---------------------------------------------------------------------------
+def _not_built(monkeypatch):
+    monkeypatch.delattr(gqa, "_fastargs", raising=False)
+    monkeypatch.setitem(sys.modules, "rope_gqa_kv_b200._fastargs", None)
+
+
+def _torch_without_the_table(monkeypatch):
+    from rope_gqa_kv_b200 import _fastargs  # noqa: F401  (it imports; torch is what lacks it)
+    monkeypatch.setattr(_lib, "torch", _TorchWithout())
+
+
+class _TorchWithout:
+    """torch, but for Tensor.__dlpack_c_exchange_api__."""
+    Tensor = type("Tensor", (), {})
+
+    def __getattr__(self, name):
+        return getattr(torch, name)
+
+
+def _another_version(monkeypatch):
+    from rope_gqa_kv_b200 import _fastargs
+
+    def setup(*args):
+        raise RuntimeError("torch's DLPack exchange table is of another version")
+    monkeypatch.setattr(_fastargs, "setup", setup)
+
+
+@pytest.mark.parametrize("lacking", [_not_built, _torch_without_the_table, _another_version])
+def test_every_entry_works_without_the_native_checks(lib, monkeypatch, lacking):
+    """The library loads, and calls go through the checks in Python."""
+    for name in ("_lib", "_fast", "_fast_pointers"):
+        monkeypatch.setattr(_lib, name, None)
+    with monkeypatch.context() as m:
+        lacking(m)
+        with pytest.warns(RuntimeWarning, match="checked in Python"):
+            other = gqa.load()
+    assert gqa.load() is other
+    assert other.gqa_prefill(None, F, F, F, 1, 16, 4, 2, 64, 128, 0.0, None, None) == 1
+    assert gqa.gqa_decode_workspace_bytes(1, 3, 64, 64) == 3 * 66 * 4
+    for call in (_lib._fast.append, _lib._fast.backward, _lib._fast.read_back, _lib._fast.decode,
+                 _lib._fast.cache, _lib._fast_pointers):
+        assert call(0, None) is None
+    with pytest.raises(ValueError, match="CUDA"):
+        gqa.Q4Cache.zeros(1, 2, 128, 64, device="cpu")
+    with pytest.raises(ValueError, match="CUDA"):
+        _lib._pointers(torch.device("cuda", 0), ("t", torch.zeros(2), torch.float32, (2,)))
+
+
+def test_native_checks_are_built_again_for_another_torch_and_may_fail(monkeypatch, tmp_path):
+    lib_path, made_for = tmp_path / "_fastargs.so", tmp_path / "fastargs.txt"
+    monkeypatch.setattr(gqa_build, "ARGS_LIB", str(lib_path))
+    monkeypatch.setattr(gqa_build, "ARGS_FOR", str(made_for))
+    gqa_build._build_args(False)
+    first = lib_path.stat().st_mtime_ns
+    gqa_build._build_args(False)
+    assert lib_path.stat().st_mtime_ns == first
+    made_for.write_text("python 3, torch 1\n")
+    gqa_build._build_args(False)
+    assert lib_path.stat().st_mtime_ns > first and torch.__version__ in made_for.read_text()
+    monkeypatch.setattr(gqa_build.shutil, "which", lambda name: "/bin/false")
+    gqa_build._build_args(False)               # nothing to do
+    with pytest.warns(RuntimeWarning, match="checked in Python"):
+        gqa_build._build_args(True)
+    assert not lib_path.exists()               # the library goes on without it
