@@ -793,14 +793,18 @@ decode_q4_merge_kernel(const float *__restrict__ ws_ml, const float *__restrict_
 // How a call is cut: heads per CTA, slots per chunk, chunks of a sequence.
 struct Plan {
     int G, n_sub, chunk, n_splits, cluster, places;
+    bool wide;                         // at most two CTAs an SM
     int most_splits;                   // n_splits of any shorter max_len, at most
 };
 
-// Calls without a second kernel ask for so much shared memory that an SM takes two CTAs,
-// which spreads their few CTAs evenly: 288 of 1024 slots (18 sequences of 2048) take 13.6 us,
-// with three on some SMs 17.7.  Against the form with a second kernel: 1 x 612 slots 3.9
-// us against 4.5 (and one launch less for the host: 5.1 against 7.4), 16 x 600 slots of 8
-// KV heads 7.7 against 11.7, 18 x 2048 13.6 against 17.9.
+// Calls whose CTAs all have a place at once (Plan::wide) ask for so much shared memory that
+// an SM takes two, which spreads them evenly: 288 of 1024 slots (18 sequences of 2048) take
+// 13.6 us, with three on some SMs 17.7.  In calls of more rounds three an SM hide more latency:
+// 256 sequences of 256 .. 2048 slots of 8 KV heads, one chunk each, 85 us against 94 with two,
+// 512 of 64 29 against 39.
+// A cluster against the form with a second kernel: 1 x 612 slots 3.9 us against 4.5 (and one
+// launch less for the host: 5.1 against 7.4), 16 x 600 slots of 8 KV heads 7.7 against 11.7,
+// 18 x 2048 13.6 against 17.9.
 constexpr int kWideSmem = 100 * 1024;
 constexpr int kClusterPlaces = 148 * 2;
 constexpr int kClusterLen = 4096;      // longer rows want more than eight chunks
@@ -815,6 +819,7 @@ Plan make_plan(int B, int Hq, int Hkv, int max_len) {
     P.G = (g + P.n_sub - 1) / P.n_sub;
     P.n_sub = (g + P.G - 1) / P.G;
     P.cluster = P.places = 0;
+    P.wide = false;
     // Few, short rows: one to eight chunks of at least 64 slots, merged within a cluster, as
     // long as all CTAs have a place at once (clusters of eight find only half of them: 32 of
     // them took 8.4 us on 4 x 1000 slots of 8 KV heads, of four 5.5) and long chunks fill
@@ -829,7 +834,8 @@ Plan make_plan(int B, int Hq, int Hkv, int max_len) {
         P.n_splits = (max_len + P.chunk - 1) / P.chunk;
         P.cluster = c > 1 ? c : 0;                         // one chunk needs none
         P.most_splits = 1;             // (shorter calls merge this way too: nothing in memory)
-        if (P.chunk <= 1024 || 8 * c * rows >= 7 * kClusterPlaces) return P;
+        P.wide = P.chunk <= 1024 || 8 * c * rows >= 7 * kClusterPlaces;
+        if (P.wide) return P;
         P.cluster = 0;
     }
     // Few rows: one chunk for each place a CTA can have, shared out by the lengths on the
@@ -876,7 +882,7 @@ size_t workspace_bytes(int B, int Hq, int D, int n_splits) {
 }
 
 template <int D, bool CLUSTER>
-cudaError_t launch_split(const DecQ4Args &A, cudaStream_t s) {
+cudaError_t launch_split(const DecQ4Args &A, bool wide, cudaStream_t s) {
     using S = DecQ4Shape<D>;
     auto kern = decode_q4_kernel<D, CLUSTER>;
     static_assert(kWideSmem >= S::kSmem, "rings");
@@ -890,7 +896,7 @@ cudaError_t launch_split(const DecQ4Args &A, cudaStream_t s) {
     cfg.gridDim = A.places ? dim3(A.Hkv * A.n_sub, 1, A.places)
                            : dim3(A.Hkv * A.n_sub, A.B, CLUSTER ? A.cluster : A.n_splits);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = CLUSTER || A.n_splits == 1 ? kWideSmem : S::kSmem;
+    cfg.dynamicSmemBytes = wide ? kWideSmem : S::kSmem;
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = CLUSTER ? 2 : 1;
@@ -913,9 +919,9 @@ cudaError_t launch_split(const DecQ4Args &A, cudaStream_t s) {
 }
 
 template <int D>
-cudaError_t launch_decode(const DecQ4Args &A, cudaStream_t s) {
-    if (A.cluster) return launch_split<D, true>(A, s);
-    const cudaError_t e = launch_split<D, false>(A, s);
+cudaError_t launch_decode(const DecQ4Args &A, bool wide, cudaStream_t s) {
+    if (A.cluster) return launch_split<D, true>(A, wide, s);
+    const cudaError_t e = launch_split<D, false>(A, wide, s);
     if (e != cudaSuccess || A.n_splits == 1) return e;
     // One warp a row while a group covers its chunks; four beyond that (65536 slots of one KV
     // head, 342 chunks: 12.2 us a call against 19.9 with one; 55 chunks: 23.2 against 23.9).
@@ -1111,8 +1117,8 @@ extern "C" gqa_status gqa_decode_q4(const void *q, const void *k_codes, const vo
     A.scale_log2 = (scale > 0.f ? scale : 1.0f / sqrtf((float)D)) * 1.4426950408889634f * 0x1p69f;
     A.slack = gqa::kSlack / A.scale_log2;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = D == 64   ? gqa::launch_decode<64>(A, s)
-                          : D == 96 ? gqa::launch_decode<96>(A, s)
-                                    : gqa::launch_decode<128>(A, s);
+    const cudaError_t e = D == 64   ? gqa::launch_decode<64>(A, P.wide, s)
+                          : D == 96 ? gqa::launch_decode<96>(A, P.wide, s)
+                                    : gqa::launch_decode<128>(A, P.wide, s);
     return e == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
 }

@@ -626,3 +626,15 @@ def test_decode_scores_of_any_size(cuda_lib, eq, ek, D, n):
             tol = 2.0 ** -8 * want.abs() + 1.01 * (2.0 ** -11 * 15 * step[at] + 80 * ref.U32 *
                                                    (15 * step[at] + low[at].abs()))
             assert ((out[b, h] - want).abs() <= tol).all(), (b, h)
+
+
+@pytest.mark.parametrize("B,Hq,Hkv,D,L,max_len", [(1300, 2, 1, 64, 128, 128),
+                                                  (160, 16, 8, 96, 256, 250),
+                                                  (400, 6, 3, 128, 128, 64)])
+def test_decode_more_rows_than_places(cuda_lib, B, Hq, Hkv, D, L, max_len):
+    """More rows than the waves of a call: one chunk each, no second kernel, many rounds."""
+    assert gqa.gqa_decode_q4_workspace_bytes(B, Hq, Hkv, D, max_len) == 16
+    lens = torch.randint(1, max_len + 1, (B,), generator=torch.Generator().manual_seed(B))
+    lens[0], lens[1], lens[2] = 1, max_len, 64
+    q = torch.randn(B, Hq, D, generator=torch.Generator().manual_seed(3)).to(BF)
+    _check_decode(q, _random_cache(B, B, Hkv, L, D), lens, max_len, "B=%d" % B)
