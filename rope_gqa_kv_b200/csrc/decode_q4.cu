@@ -725,7 +725,7 @@ decode_q4_merge_kernel(const float *__restrict__ ws_ml, const float *__restrict_
         const bool mine = lane < B;
         chunk = even_chunk(mine ? len_or_zero(lens, lane, max_len, Lmax) : 0, mine, B, places);
     }
-    const int ns = (len + chunk - 1) / chunk;
+    const int ns = (len - 1) / chunk + 1;                  // len + chunk may pass 2^31
     const float *ml = ws_ml + (size_t)row * n_splits * 2;
     const float *po = ws_o + (size_t)row * n_splits * D + lane * 4;
     float M = -INFINITY, L = 0.f;
@@ -870,7 +870,7 @@ Plan make_plan(int B, int Hq, int Hkv, int max_len) {
     const long long slots = rows * max_len;
     const long long even = ((long long)((double)slots / (kPlaces * kWaves)) + 63) / 64 * 64;
     P.chunk = (int)(even < 64 ? 64 : even > 64LL * most ? 64LL * most : even);
-    P.n_splits = (max_len + P.chunk - 1) / P.chunk;
+    P.n_splits = (max_len - 1) / P.chunk + 1;
     return P;
 }
 

@@ -327,3 +327,15 @@ def test_native_checks_are_built_again_for_another_torch_and_may_fail(monkeypatc
     with pytest.warns(RuntimeWarning, match="checked in Python"):
         gqa_build._build_args(True)
     assert not lib_path.exists()               # the library goes on without it
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the call goes on to its launch")
+@pytest.mark.parametrize("n", [(1 << 30) + 1, (1 << 31) - (1 << 21), (1 << 31) - 128])
+def test_decode_q4_takes_the_longest_caches(lib, n):
+    """A cache of 2^31 slots of one head of 64 fits the device: chunk counts do not pass 2^31
+    on the way.  Without a device an accepted call fails at its launch (5)."""
+    size = lib.gqa_decode_q4_workspace_bytes(1, 2, 1, 64, n)
+    assert size >= 1184 * 2 * 66 * 4
+    for ws_bytes, want in ((size, 5), (16, 6)):
+        assert lib.gqa_decode_q4(F, F, F, F, F, F, n, F, 1, 2, 1, 64, (1 << 31) - 128, 0.0, F,
+                                 ws_bytes, None, None) == want
