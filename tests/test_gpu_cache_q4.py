@@ -638,3 +638,27 @@ def test_decode_more_rows_than_places(cuda_lib, B, Hq, Hkv, D, L, max_len):
     lens[0], lens[1], lens[2] = 1, max_len, 64
     q = torch.randn(B, Hq, D, generator=torch.Generator().manual_seed(3)).to(BF)
     _check_decode(q, _random_cache(B, B, Hkv, L, D), lens, max_len, "B=%d" % B)
+
+
+@pytest.mark.parametrize("B,Hq,Hkv,D,lengths", [
+    (8, 8, 8, 64, [4800, 4736, 4097, 4096, 1500, 64, 1]),      # waves, clusters
+    (3, 6, 2, 128, [9088, 9000, 5000, 4160, 4090, 100]),       # shared out by the lengths, clusters
+    (40, 8, 4, 96, [1280, 1279, 600, 65]),                     # clusters of two, one chunk
+    (125, 8, 8, 64, [384, 320, 129, 64]),                      # waves of many rows
+    (1, 2, 1, 64, [33024, 33000, 20000, 4097, 4096])])
+def test_one_workspace_for_the_capacity_and_every_shorter_call(cuda_lib, B, Hq, Hkv, D, lengths):
+    """The workspace of the longest call, between guard bytes, serves the others: the
+    answers are right, and nothing outside of it is written."""
+    L = (lengths[0] + 127) // 128 * 128
+    size, guard = gqa.gqa_decode_q4_workspace_bytes(B, Hq, Hkv, D, lengths[0]), 4096
+    buf = torch.empty(guard + size + guard, dtype=torch.uint8, device=DEV)
+    parts = _random_cache(B + D, B, Hkv, L, D)
+    g = torch.Generator().manual_seed(size % 1000)
+    q = torch.randn(B, Hq, D, generator=g).to(BF)
+    for n in lengths:
+        assert gqa.gqa_decode_q4_workspace_bytes(B, Hq, Hkv, D, n) <= size
+        lens = torch.randint(1, n + 1, (B,), generator=g)
+        lens[-1] = n
+        buf.fill_(0xFF)                        # NaN wherever it is read as fp32
+        _check_decode(q, parts, lens, n, "max_len=%d" % n, workspace=buf[guard:guard + size])
+        assert (buf[:guard] == 0xFF).all() and (buf[guard + size:] == 0xFF).all()
