@@ -150,17 +150,6 @@ __device__ __forceinline__ void store_remote(uint32_t at, float x, float y) {
     asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(at), "f"(x), "f"(y) : "memory");
 }
 
-// 16 bytes, global to shared, the last 16 - n of them zeros; counted by commit groups.
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, int n = 16) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
-                 : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 template <int D>
 struct DecQ4Shape {
     static constexpr int NG = Q4Shape<D>::NG;
@@ -1011,20 +1000,6 @@ read_q4_kernel(const ReadArgs A) {
     }
 }
 
-template <int D>
-cudaError_t launch_read(const ReadArgs &A, int B, cudaStream_t s) {
-    cudaLaunchAttribute pdl[1];
-    pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    pdl[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((A.Lout + kReadRows - 1) / kReadRows), A.Hkv, B);
-    cfg.blockDim = dim3(kThreads);
-    cfg.stream = s;
-    cfg.attrs = pdl;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, read_q4_kernel<D>, A);
-}
-
 }  // namespace
 }  // namespace gqa
 
@@ -1058,9 +1033,11 @@ extern "C" gqa_status kv_cache_read_q4(const void *k_codes, const void *k_scales
     A.Lmax = Lmax;
     A.Lout = Lout;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = D == 64   ? gqa::launch_read<64>(A, B, s)
-                          : D == 96 ? gqa::launch_read<96>(A, B, s)
-                                    : gqa::launch_read<128>(A, B, s);
+    const auto kern = D == 64   ? gqa::read_q4_kernel<64>
+                      : D == 96 ? gqa::read_q4_kernel<96>
+                                : gqa::read_q4_kernel<128>;
+    const dim3 grid((unsigned)((Lout - 1) / gqa::kReadRows + 1), Hkv, B);
+    const cudaError_t e = gqa::launch_pdl(kern, grid, gqa::kThreads, s, A);
     return e == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
 }
 

@@ -169,16 +169,6 @@ __device__ __forceinline__ void turn_vector(uint4 &a, uint4 &b, const Turn &t, b
     b = make_uint4(ob[0], ob[1], ob[2], ob[3]);
 }
 
-// 16 bytes, global to shared; counted by commit groups.
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 // A warp's way through its units -- unit, unit + stride, .. -- a unit being a slice of a
 // token's passes: the slice, its token t of sequence b.  The steps are taken without a
 // division.

@@ -29,7 +29,6 @@ template <int D>
 struct Q4Shape {
     static constexpr int NG = D / 32;             // groups of a row
     static constexpr int kCodeBytes = D / 2;
-    static constexpr int kScaleBytes = 4 * NG;
 };
 
 // 2^-126 as fp32: smaller steps are not kept.

@@ -67,15 +67,12 @@ __device__ __forceinline__ void lane_angles(const float *cs_row, const float *sn
     }
 }
 
-// RMSNorm (if qk_norm) and rotation of the lane's 16 coordinates.  With GAIN the
-// normalised coordinates are multiplied by gain[0 .. 7] (the lane's chunk of the
-// first half) and gain[D/2 ..] (the matching chunk of the second) before turning;
-// a gain of one gives the bits of the version without.
-template <int D, bool GAIN = false>
+// RMSNorm (if qk_norm) and rotation of the lane's 16 coordinates.
+template <int D>
 __device__ __forceinline__ void rotate_vector(const uint4 a_in, const uint4 b_in, uint4 &a_out,
                                               uint4 &b_out, const float (&c)[8],
                                               const float (&sv)[8], bool active, bool qk_norm,
-                                              float eps, const float *gain = nullptr) {
+                                              float eps) {
     using S = RopeShape<D>;
     float xa[8], xb[8];
     const uint32_t wa[4] = {a_in.x, a_in.y, a_in.z, a_in.w};
@@ -103,19 +100,6 @@ __device__ __forceinline__ void rotate_vector(const uint4 a_in, const uint4 b_in
         for (int e = 0; e < 8; e += 2) {
             mul2(xa[e], xa[e + 1], xa[e], xa[e + 1], inv, inv);
             mul2(xb[e], xb[e + 1], xb[e], xb[e + 1], inv, inv);
-        }
-        if constexpr (GAIN) {
-            if (active) {
-#pragma unroll
-                for (int e = 0; e < 8; e += 4) {
-                    const float4 ga = *reinterpret_cast<const float4 *>(gain + e);
-                    const float4 gb = *reinterpret_cast<const float4 *>(gain + S::kHalf + e);
-                    mul2(xa[e], xa[e + 1], xa[e], xa[e + 1], ga.x, ga.y);
-                    mul2(xa[e + 2], xa[e + 3], xa[e + 2], xa[e + 3], ga.z, ga.w);
-                    mul2(xb[e], xb[e + 1], xb[e], xb[e + 1], gb.x, gb.y);
-                    mul2(xb[e + 2], xb[e + 3], xb[e + 2], xb[e + 3], gb.z, gb.w);
-                }
-            }
         }
     }
     // rotation of pairs (8j + 2e, 8j + 2e + 1) two at a time:
