@@ -7,8 +7,10 @@
 // stands for m + s c:
 //     m = min x,   s = bf16((max x - m) / 15),   c = ceil((x - m) / s - 1/2).
 // The values quantised are bf16, so m is exact; rounding s to 8 bits moves the
-// largest value's quotient by at most 15 * 2^-8 = 0.06, so no code is clipped and
-// |m + s c - x| <= s/2 holds for every value.  A group with s below 2^-126 keeps
+// largest value's quotient by at most 15 * 2^-8 = 0.06, so no code is clipped.  With
+// the formula's codes |m + s c - x| <= s/2 for every value; q4_quantise lets a quotient
+// less than 2^-19 of itself above n + 1/2 fall to n, which adds that share of the
+// quotient times s, 15 * 2^-19 s at most.  A group with s below 2^-126 keeps
 // s = 0 (all values m); one that holds a value that is not finite keeps m = NaN,
 // s = 0: all its values read back as NaN.
 //
@@ -65,9 +67,10 @@ __device__ __forceinline__ void q4_fma2(float &d0, float &d1, float a0, float a1
 // fused operation, exact whenever the difference fits 24 bits.  The quotient is
 // t * (2/s) with 2/s made smaller by 2^-21 of itself: a quotient that is exactly
 // n + 1/2 then lands below it by more than the rounding errors (2^-23) and rounds
-// down to n, as the formula asks, and the nearest other quotients two bf16
-// operands can form lie far outside that margin.  Adding 1.5 * 2^23 in the same
-// fused operation leaves the rounded code in the low bits of the sum.
+// down to n, as the formula asks.  So does one that lies above n + 1/2 by less than
+// that margin: x - m, of two bf16 values, can have more bits than fp32 (m = -s/2 and
+// x = 2^-30 s have the quotient 1/2 + 2^-30, whose code would be 1).  Adding 1.5 * 2^23
+// in the same fused operation leaves the rounded code in the low bits of the sum.
 __device__ __forceinline__ void q4_quantise(const uint4 a, const uint4 b, uint32_t (&codes)[2],
                                             uint32_t &sm) {
     const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
