@@ -662,3 +662,35 @@ def test_one_workspace_for_the_capacity_and_every_shorter_call(cuda_lib, B, Hq, 
         buf.fill_(0xFF)                        # NaN wherever it is read as fp32
         _check_decode(q, parts, lens, n, "max_len=%d" % n, workspace=buf[guard:guard + size])
         assert (buf[:guard] == 0xFF).all() and (buf[guard + size:] == 0xFF).all()
+
+
+@pytest.mark.parametrize("D,n", [(64, 262144), (96, 131072), (128, 131072)])
+def test_decode_sums_of_long_chunks(cuda_lib, D, n):
+    """Chunks of 10000 to 20000 keys with equal weights (q = 0).  V's minima take the mean of
+    its codes away to 1/4000, so a sum that loses 2^-15 of what it adds up is off by 10 % of
+    the answer.  Everything up to the chunks' merge is exact in fp32 by choice of the steps
+    (255/128 times a power of two) but for 2^-8 in sums that pass 2^16, a few times in 5000
+    keys: 1e-5 of the step's power covers it and the merge, beside the rounding to bf16."""
+    Hkv, ng = 32, D // 32
+    g = torch.Generator(device=DEV).manual_seed(n + D)
+    codes = [torch.randint(0, 256, (1, Hkv, n, D // 2), generator=g, dtype=torch.uint8, device=DEV)
+             for _ in range(2)]
+    power = torch.exp2(3.0 * torch.arange(ng, device=DEV))
+    low = torch.where(torch.arange(n, device=DEV) % 2 == 0, -15.0, -14.875).view(n, 1) * power
+    sv = torch.stack((power.expand(n, ng) * (255 / 128), low), -1).to(BF)
+    sv = sv.expand(1, Hkv, n, ng, 2).contiguous()
+    sk = torch.zeros_like(sv)
+    cache = gqa.Q4Cache(codes[0], sk, codes[1], sv)
+    q = torch.zeros(1, Hkv, D, dtype=BF, device=DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    lens = torch.full((1,), n, dtype=torch.int32, device=DEV)
+    out = gqa.gqa_decode_q4(q, cache, lens, n, status=status)[0].double()
+    assert status.item() == 0
+    grp = (torch.arange(D, device=DEV) % (D // 2)) // 16
+    for h in range(Hkv):
+        c = ref.unpack_codes(codes[1][0, h]).double().mean(0)
+        want = (c * (255 / 128) - 14.9375) * power.double()[grp]
+        tol = 2.0 ** -8 * want.abs() + 1e-5 * power.double()[grp]
+        d = (out[h] - want).abs()
+        assert (d <= tol).all(), "head %d: %.3g of the bound" % (h, float((d / tol).max()))
+    cache = codes = sv = sk = None
