@@ -89,23 +89,28 @@ class DecodeGraph:
                                       **learned, **args)
             _lib.gqa_decode(q_rot, k_cache, v_cache, self._lens[b], self.max_len, **tail)
 
-        # One eager step first, on a side stream, so that every first-use setup
-        # (kernel attributes, the library load) happens outside the capture.  It
-        # writes only the cache slot at each sequence's current length -- the
-        # slot the first real step overwrites -- and the second length vector.
-        side = torch.cuda.Stream(device=dev)
-        side.wait_stream(torch.cuda.current_stream(dev))
-        with torch.cuda.stream(side):
-            one_step(0, 1)
-        torch.cuda.current_stream(dev).wait_stream(side)
-        torch.cuda.synchronize(dev)
-        self.status.zero_()
-        self._graphs = []
-        for a, b in ((0, 1), (1, 0)):
-            g = torch.cuda.CUDAGraph()
-            with torch.cuda.graph(g):
-                one_step(a, b)
-            self._graphs.append(g)
+        # A capture takes what is launched on its stream, by default one of the device that
+        # was current at the process's first capture: with the caches on another one the
+        # launches would go by the graph.
+        self._device = dev
+        with torch.cuda.device(dev):
+            # One eager step first, on a side stream, so that every first-use setup
+            # (kernel attributes, the library load) happens outside the capture.  It
+            # writes only the cache slot at each sequence's current length -- the
+            # slot the first real step overwrites -- and the second length vector.
+            side = torch.cuda.Stream(device=dev)
+            side.wait_stream(torch.cuda.current_stream(dev))
+            with torch.cuda.stream(side):
+                one_step(0, 1)
+            torch.cuda.current_stream(dev).wait_stream(side)
+            torch.cuda.synchronize(dev)
+            self.status.zero_()
+            self._graphs = []
+            for a, b in ((0, 1), (1, 0)):
+                g = torch.cuda.CUDAGraph()
+                with torch.cuda.graph(g, stream=side):
+                    one_step(a, b)
+                self._graphs.append(g)
         self._cur = 0           # index of the length vector that holds the current lengths
 
     @property
@@ -114,6 +119,10 @@ class DecodeGraph:
 
     def step(self) -> torch.Tensor:
         """Append the token in q, k, v at the current lengths and decode it."""
-        self._graphs[self._cur].replay()
+        if torch.cuda.current_device() == self._device.index:
+            self._graphs[self._cur].replay()
+        else:
+            with torch.cuda.device(self._device):
+                self._graphs[self._cur].replay()
         self._cur ^= 1
         return self.out

@@ -694,3 +694,39 @@ def test_decode_sums_of_long_chunks(cuda_lib, D, n):
         d = (out[h] - want).abs()
         assert (d <= tol).all(), "head %d: %.3g of the bound" % (h, float((d / tol).max()))
     cache = codes = sv = sk = None
+
+
+@pytest.mark.parametrize("q4", [True, False])
+def test_decode_graph_captures_and_replays_on_the_caches_device(cuda_lib, monkeypatch, q4):
+    """Whichever device is current (here one that does not exist, as far as DecodeGraph can
+    see), the capture's stream and the replay's are the caches' device's."""
+    B, Hq, Hkv, D, L = 2, 4, 2, 64, 128
+    g = torch.Generator().manual_seed(60)
+    new = lambda *s: torch.randn(*s, generator=g).to(BF).to(DEV)
+    caches = (gqa.Q4Cache.zeros(B, Hkv, L, D), None) if q4 else (new(B, Hkv, L, D), new(B, Hkv, L, D))
+    lens = torch.tensor([3, 60], dtype=torch.int32, device=DEV)
+    entered, captured = [], []
+    real_device, real_graph = torch.cuda.device, torch.cuda.graph
+
+    class Device(real_device):
+        def __enter__(self):
+            entered.append(self.idx)
+            return super().__enter__()
+
+    def graph(cuda_graph, **kw):
+        captured.append(kw["stream"].device)
+        return real_graph(cuda_graph, **kw)
+
+    with monkeypatch.context() as m:
+        m.setattr(torch.cuda, "device", Device)
+        m.setattr(torch.cuda, "graph", graph)
+        dg = gqa.DecodeGraph(*caches, lens, Hq, qk_norm=True)
+        assert captured == [lens.device] * 2 and lens.device.index in entered
+        dg.q.copy_(new(B, Hq, D)), dg.k.copy_(new(B, Hkv, D)), dg.v.copy_(new(B, Hkv, D))
+        del entered[:]
+        m.setattr(torch.cuda, "current_device", lambda: lens.device.index + 1)
+        out = dg.step()
+        assert entered == [lens.device.index]
+    torch.cuda.synchronize()
+    assert dg.lens.tolist() == [4, 61] and dg.status.item() == 0
+    assert torch.isfinite(out).all() and out.abs().amax(-1).gt(0).all()
