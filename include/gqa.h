@@ -435,8 +435,9 @@ gqa_status kv_cache_read_q4(const void *k_codes, const void *k_scales, const voi
  * there; gqa_decode_q4_workspace_bytes gives its size, which serves every shorter
  * max_len_host too (16 bytes where all of these merge without it).
  * The chunks' length follows from B, the heads and max_len_host, and with few rows
- * from all lens too: equal calls give equal bits.  Queries and values
- * of magnitude up to 2^60 and 2^110 are handled (sums of larger ones can overflow).
+ * from all lens too: equal calls give equal bits.  Queries of magnitude up to
+ * 2^60, any finite keys and values of magnitude up to 2^110 are handled (sums of larger
+ * ones can overflow).
  */
 gqa_status gqa_decode_q4(const void *q, const void *k_codes, const void *k_scales,
                          const void *v_codes, const void *v_scales, const int32_t *lens,

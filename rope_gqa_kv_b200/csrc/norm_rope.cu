@@ -370,8 +370,9 @@ norm_rope_append_kernel(const AppendArgs A, const __grid_constant__ RopeTable ta
 // rows in a fixed order, so equal calls give equal bits.
 //
 // Measured on 8 x 2048 tokens of 24 / 8 heads, D = 128 (470 MB, 72 us at the copy rate):
-// 81 us, 88 % of it; 4 CTAs an SM at fewer registers 97 us; 3 x 1001 tokens of 8 / 8
-// heads, D = 96 (5.6 us) 16.8 us, 3 of them the second kernel.
+// 82 to 90 us from GPU to GPU, 80 to 88 % of it; 4 CTAs an SM at fewer registers 97 us where
+// this takes 82; 3 x 1001 tokens of 8 / 8 heads, D = 96 (5.6 us) 17 us, 3 of them the second
+// kernel.
 constexpr int kBwdWarps = 4;
 constexpr int kBwdResident = 3;                            // CTAs per SM
 constexpr int kBwdMaxCtas = 148 * kBwdResident;

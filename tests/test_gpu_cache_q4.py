@@ -589,10 +589,11 @@ def test_the_checks_in_python_lead_to_the_same_calls(cuda_lib, monkeypatch):
         assert all(torch.equal(x, y) for x, y in zip(got, want))
 
 
-@pytest.mark.parametrize("eq,ek", [(12, 0), (28, 0), (31, 0), (40, 0), (60, 0), (60, 50)])
+@pytest.mark.parametrize("eq,ek", [(12, 0), (28, 0), (31, 0), (40, 0), (60, 0), (60, 50),
+                                   (60, 110)])
 @pytest.mark.parametrize("D,n", [(64, 100), (96, 700), (128, 4500)])
 def test_decode_scores_of_any_size(cuda_lib, eq, ek, D, n):
-    """Scores of up to +-2^118, exact in fp32, all of one sign: q has one coordinate, +-2^eq,
+    """Scores of up to +-2^178, exact in float64, all of one sign: q has one coordinate, +-2^eq,
     and K's rows are constants 2^ek times 141 .. 239 with one 255 (which takes all of the
     heads with a positive q) and one 128 (the others': their scores are all negative)."""
     B, Hq, Hkv, L = 2, 4, 2, (n + 127) // 128 * 128
