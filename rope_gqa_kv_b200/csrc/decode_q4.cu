@@ -28,7 +28,7 @@
 //     sum(p m) is added up in fp32 beside it.
 //   * the codes are all positive and the minima take most of their sum away again, while
 //     the tensor cores cut every product off at the last place of the sum so far: over
-//     a long chunk a loss of 2^-22 of the sum for every 16 keys, all one way.  Every
+//     a long chunk a loss of some 2^-23 of the sum so far for every 16 keys, all one way.  Every
 //     kCentre units the sums are therefore moved past zero by what one coordinate has
 //     gathered, and that amount goes over to sum(p m): neither changes the result, and the
 //     loss no longer grows with the chunk.
