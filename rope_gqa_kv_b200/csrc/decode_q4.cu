@@ -26,9 +26,9 @@
 //     bf16's 2^-8 (terms below 2^-19 of the group's largest lose bits, 2^-30 of it at
 //     most).
 //     sum(p m) is added up in fp32 beside it.
-//   * the codes are all positive and the minima take most of their sum away again, while
+//   * the codes are never negative and the minima take most of their sum away again, while
 //     the tensor cores cut every product off at the last place of the sum so far: over
-//     a long chunk a loss of some 2^-23 of the sum so far for every 16 keys, all one way.  Every
+//     a long chunk a loss of some 2^-23 of that sum for every 16 keys, all one way.  Every
 //     kCentre units the sums are therefore moved past zero by what one coordinate has
 //     gathered, and that amount goes over to sum(p m): neither changes the result, and the
 //     loss no longer grows with the chunk.
